@@ -265,6 +265,169 @@ muon_status muon_debug_square_buffer(const muon_param *params, int n, int ns_ste
                                      int index, int which,
                                      size_t *offset, int64_t *ld, int64_t *side);
 
+/* ---------------------------------------------------------------------------
+ * Training operators around the step: where the gradients that muon_step and
+ * muon_adamw_step take come from.
+ *
+ * 8-bit activation checkpoints.  A row-major rows x cols activation x is kept
+ * in blocks of MUON_CKPT_BLOCK consecutive columns of a row (the last block of
+ * a row may be shorter).  A block with a = max |x| stores one exponent byte
+ * b and one code q per value, and stands for x^ = q 2^(b - 127):
+ *     b = e + 127, e the smallest integer >= -111 with a <= Q 2^e,
+ *     q = x 2^-e rounded to nearest even on the code's grid,
+ * with Q = 448 and the e4m3 grid (MUON_E4M3: sign, 4 exponent bits of bias 7,
+ * 3 fraction bits, no infinities) or Q = 127 and whole numbers (MUON_INT8).
+ * x^ is exact in fp32 and bf16; in fp16 it is rounded to nearest, and finite
+ * values beyond the range become +-65504.  |x| above Q 2^(127 - floor(log2 Q))
+ * (0.992 or 0.875 of 2^128) is stored as that value.  A block that holds an
+ * infinity or NaN stores b = 255 and codes 0, and stands for NaN throughout.
+ *
+ * For every entry point below: matrices are row-major with unit column stride
+ * and a row stride `ld` in elements; bases and row strides need no alignment
+ * beyond the element's own (codes excepted).  An output may not overlap any
+ * other buffer of the call; rows of two outputs may interleave (two halves of
+ * one wider matrix).  rows == 0 is a no-op wherever it leaves nothing to
+ * write.  The calls allocate nothing, can be captured in a HIP graph, and are
+ * bitwise reproducible.  Errors are those of muon_step. */
+#define MUON_CKPT_BLOCK 32
+
+typedef enum muon_ckpt_format { MUON_E4M3 = 0, MUON_INT8 = 1 } muon_ckpt_format;
+
+typedef struct muon_ckpt {
+  uint8_t *codes;       /* rows x codes_ld bytes, 16-byte aligned; codes_ld a multiple of 16, >= cols.
+                           Bytes past cols up to the next multiple of 16 are
+                           written as 0 and may be read; later ones are not touched */
+  uint8_t *scales;      /* rows x scales_ld bytes, scales_ld >= ceil(cols / MUON_CKPT_BLOCK) */
+  int64_t rows, cols;   /* rows >= 0, 1 <= cols <= 2^20                                  */
+  int64_t codes_ld, scales_ld;
+  muon_ckpt_format format;
+} muon_ckpt;
+
+/* ckpt <- x (rows x cols of `dtype`, as ckpt says). */
+muon_status muon_ckpt_pack(const void *x, int64_t ld, muon_dtype dtype, const muon_ckpt *ckpt, void *stream);
+
+/* x <- the values the checkpoint stands for, rounded to `dtype`. */
+muon_status muon_ckpt_unpack(const muon_ckpt *ckpt, void *x, int64_t ld, muon_dtype dtype, void *stream);
+
+/* SwiGLU with its two inputs kept in 8 bits, in one pass:
+ *     h = gate * sigmoid(gate) * up     (fp32 arithmetic, rounded once to dtype)
+ * and gate_ckpt <- gate, up_ckpt <- up.  Both checkpoints have h's rows and
+ * cols and one format. */
+muon_status muon_ckpt_swiglu(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, muon_dtype dtype,
+                             void *h, int64_t ld_h, const muon_ckpt *gate_ckpt, const muon_ckpt *up_ckpt,
+                             void *stream);
+
+/* Its backward pass out of the checkpoints, with g, u the values they stand
+ * for and s = sigmoid(g):
+ *     grad_gate = grad_h u s (1 + g (1 - s)),  grad_up = grad_h g s,
+ *     h = g s u   (optional, NULL => not written; what the next projection's
+ *                  weight gradient takes)
+ * all of `dtype`, fp32 arithmetic, rounded once. */
+muon_status muon_ckpt_swiglu_backward(const void *grad_h, int64_t ld_grad_h, muon_dtype dtype, const muon_ckpt *gate_ckpt,
+                                      const muon_ckpt *up_ckpt, void *grad_gate, int64_t ld_grad_gate, void *grad_up,
+                                      int64_t ld_grad_up, void *h, int64_t ld_h, void *stream);
+
+/* Weight gradients out of a checkpoint of the layer's input, one matrix or
+ * one for each expert:
+ *     dW_e[n][d] = sum over i in [offsets[e], offsets[e + 1]) of
+ *                  grad_y[i][n] * x^[rows_of[i]][d]
+ * (offsets == NULL: one matrix, every i; rows_of == NULL: row i of the
+ * checkpoint), written as outs x cols (grad of a weight stored [out, in]) or,
+ * transposed, as cols x outs.  grad_y and x^ meet as 16-bit matrix operands of
+ * grad_y's dtype (x^ exact in bf16); sums are held in fp32 and rounded once to
+ * out_dtype, which is what muon_step takes as `grad`.  accumulate: dW is
+ * added to what `out` holds.  An expert without rows gets zeros (or stays as
+ * it is).  offsets[e] is read clamped to [0, slots] and offsets[e + 1] to
+ * [offsets[e], slots], and a slot whose rows_of entry lies outside
+ * [0, ckpt.rows) is left out, so device lists are never followed out of
+ * range. */
+typedef struct muon_wgrad {
+  const void *grad_y;         /* slots x outs                                        */
+  int64_t ld_grad_y;
+  int64_t slots;              /* >= 0; equal to ckpt.rows when rows_of == NULL        */
+  int64_t outs;               /* 1 <= outs <= 2^20                                    */
+  muon_dtype dtype;           /* of grad_y: F16 or BF16                               */
+  muon_ckpt ckpt;             /* the layer's input, read only                         */
+  int32_t experts;            /* >= 1; 1 when offsets == NULL                         */
+  int32_t transposed;         /* 0: out[n][d]; else out[d][n]                         */
+  const int32_t *offsets;     /* DEVICE int32 [experts + 1], or NULL                  */
+  const int32_t *rows_of;     /* DEVICE int32 [slots], or NULL                        */
+  void *out;                  /* experts matrices, contiguous one after another       */
+  muon_dtype out_dtype;
+  int32_t accumulate;
+} muon_wgrad;
+
+/* Device bytes of workspace muon_ckpt_wgrad needs for this call (never 0 for a
+ * valid one); 0 when the request is invalid.  Depends only on shapes and
+ * settings. */
+size_t muon_ckpt_wgrad_workspace_size(const muon_wgrad *args);
+muon_status muon_ckpt_wgrad(const muon_wgrad *args, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Routing of tokens to experts.  Per token, with l its row of logits:
+ *     s = softmax(l) or sigmoid(l);   choice c = s + bias (bias == NULL: the
+ *     logits themselves order the experts);
+ *     with top_groups < groups, experts come in `groups` runs of equal length:
+ *     a run scores the sum of its group_top (1 or 2) best s + bias, the
+ *     top_groups best runs stay, the others' experts are out;
+ *     the top_k best experts by choice, best first, are taken;
+ *     weight = scale * s, divided by the sum of the taken s when `renormalize`
+ *     (0 when that sum is 0).
+ * Choices are decided as in 64-bit arithmetic; equal ones go to the lowest
+ * index.  A logit of -inf makes the choice -inf; an expert whose choice is -inf
+ * or NaN is never taken, and a token with fewer than top_k others gets id -1
+ * and weight 0 in the places left.  A token with token_mask == 0 gets ids -1 and weights 0, one
+ * whose scores hold a NaN ids -1 and weights NaN.
+ *
+ * Dispatch lists (all of them or none): counts[e] taken slots of expert e,
+ * offsets their exclusive prefix sums, order the flat slots t * top_k + j
+ * grouped by expert, ascending within one, and rows their tokens t (what
+ * muon_wgrad.rows_of takes).  Entries from offsets[experts] on hold -1.
+ * load, when given, gets counts added to it. */
+typedef enum muon_score { MUON_SOFTMAX = 0, MUON_SIGMOID = 1 } muon_score;
+
+typedef struct muon_routing {
+  const void *logits;         /* tokens x experts of `dtype`                          */
+  int64_t ld_logits;
+  int64_t tokens;             /* >= 0, tokens * top_k < 2^31                          */
+  muon_dtype dtype;
+  int32_t experts;            /* 1 .. 1024                                            */
+  int32_t top_k;              /* 1 .. 64, <= experts of the groups that stay          */
+  muon_score score;
+  int32_t groups;             /* >= 1, divides experts, <= 64 when top_groups < groups */
+  int32_t top_groups;         /* 1 .. groups                                          */
+  int32_t group_top;          /* 1 or 2                                               */
+  int32_t renormalize;
+  float scale;
+  const float *bias;          /* fp32 [experts], or NULL                              */
+  const uint8_t *token_mask;  /* [tokens], 0: no token there; or NULL                 */
+  int32_t *expert_ids;        /* tokens x top_k, out                                  */
+  float *weights;             /* tokens x top_k, out                                  */
+  int32_t *counts;            /* [experts], out          -- all four or none           */
+  int32_t *offsets;           /* [experts + 1], out                                   */
+  int32_t *order;             /* [tokens * top_k], out                                */
+  int32_t *rows;              /* [tokens * top_k], out                                */
+  int64_t *load;              /* [experts], added to, or NULL; needs the lists        */
+} muon_routing;
+
+size_t muon_route_workspace_size(const muon_routing *args);
+muon_status muon_route(const muon_routing *args, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradient of the weights above with respect to the logits, the chosen
+ * experts held fixed: grad_weights is tokens x top_k fp32, grad_logits
+ * tokens x experts of `dtype`.  Of `args` logits, ld_logits, tokens, dtype,
+ * experts, top_k, score, renormalize, scale and expert_ids (read) are used.
+ * Ids outside [0, experts) carry no gradient (a token without experts gets
+ * zeros); an id that occurs twice adds twice. */
+muon_status muon_route_backward(const muon_routing *args, const float *grad_weights, void *grad_logits, int64_t ld_grad_logits,
+                                void *stream);
+
+/* Balance of the experts by their bias, which takes no gradient: per layer
+ *     bias[e] += rate * sign(mean over experts of counts - counts[e])
+ * (compared in whole numbers).  bias and counts are layers x experts,
+ * contiguous; counts is int32 (count_bytes 4) or int64 (8), each >= 0. */
+muon_status muon_balance_step(float *bias, const void *counts, int count_bytes, int64_t layers, int64_t experts, float rate,
+                              void *stream);
+
 /* Static description of a status code. */
 const char *muon_status_string(muon_status s);
 

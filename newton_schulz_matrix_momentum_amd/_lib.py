@@ -24,8 +24,15 @@ MUON_ERR_HIP = 4
 MUON_F32, MUON_F16, MUON_BF16 = 0, 1, 2
 MUON_NS_DIRECT, MUON_NS_GRAM, MUON_LIMUON = 0, 1, 2
 
+MUON_E4M3, MUON_INT8 = 0, 1
+MUON_SOFTMAX, MUON_SIGMOID = 0, 1
+CKPT_BLOCK = 32   # MUON_CKPT_BLOCK
+
 # every entry point declared in include/muon.h
 EXPORTS = ("muon_options_init", "muon_workspace_size", "muon_step", "muon_step_static", "muon_adamw_step",
+           "muon_ckpt_pack", "muon_ckpt_unpack", "muon_ckpt_swiglu", "muon_ckpt_swiglu_backward",
+           "muon_ckpt_wgrad", "muon_ckpt_wgrad_workspace_size", "muon_route", "muon_route_workspace_size",
+           "muon_route_backward", "muon_balance_step",
            "muon_debug_square_buffer", "muon_status_string", "muon_last_error", "muon_version")
 # bytes of the static workspace of muon_step_static (MUON_STATIC_WORKSPACE_BYTES)
 STATIC_WORKSPACE_BYTES = 64 << 20
@@ -91,6 +98,62 @@ class MuonAdamwParam(ctypes.Structure):
     ]
 
 
+class MuonCkpt(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("codes_ld", ctypes.c_int64),
+        ("scales_ld", ctypes.c_int64),
+        ("format", ctypes.c_int),
+    ]
+
+
+class MuonWgrad(ctypes.Structure):
+    _fields_ = [
+        ("grad_y", ctypes.c_void_p),
+        ("ld_grad_y", ctypes.c_int64),
+        ("slots", ctypes.c_int64),
+        ("outs", ctypes.c_int64),
+        ("dtype", ctypes.c_int),
+        ("ckpt", MuonCkpt),
+        ("experts", ctypes.c_int32),
+        ("transposed", ctypes.c_int32),
+        ("offsets", ctypes.c_void_p),
+        ("rows_of", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("out_dtype", ctypes.c_int),
+        ("accumulate", ctypes.c_int32),
+    ]
+
+
+class MuonRouting(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p),
+        ("ld_logits", ctypes.c_int64),
+        ("tokens", ctypes.c_int64),
+        ("dtype", ctypes.c_int),
+        ("experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("score", ctypes.c_int),
+        ("groups", ctypes.c_int32),
+        ("top_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("bias", ctypes.c_void_p),
+        ("token_mask", ctypes.c_void_p),
+        ("expert_ids", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
+        ("counts", ctypes.c_void_p),
+        ("offsets", ctypes.c_void_p),
+        ("order", ctypes.c_void_p),
+        ("rows", ctypes.c_void_p),
+        ("load", ctypes.c_void_p),
+    ]
+
+
 class MuonError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__("libmuon: %s (status %d)" % (message, status))
@@ -135,6 +198,23 @@ def load(path: str = LIB_PATH):
                                              ctypes.POINTER(ctypes.c_size_t), ctypes.POINTER(ctypes.c_int64),
                                              ctypes.POINTER(ctypes.c_int64)]
     lib.muon_debug_square_buffer.restype = ctypes.c_int
+    ptr, i64, ckpt = ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(MuonCkpt)
+    for name, args in {
+        "muon_ckpt_pack": [ptr, i64, ctypes.c_int, ckpt, ptr],
+        "muon_ckpt_unpack": [ckpt, ptr, i64, ctypes.c_int, ptr],
+        "muon_ckpt_swiglu": [ptr, i64, ptr, i64, ctypes.c_int, ptr, i64, ckpt, ckpt, ptr],
+        "muon_ckpt_swiglu_backward": [ptr, i64, ctypes.c_int, ckpt, ckpt, ptr, i64, ptr, i64, ptr, i64, ptr],
+        "muon_ckpt_wgrad": [ctypes.POINTER(MuonWgrad), ptr, ctypes.c_size_t, ptr],
+        "muon_route": [ctypes.POINTER(MuonRouting), ptr, ctypes.c_size_t, ptr],
+        "muon_route_backward": [ctypes.POINTER(MuonRouting), ptr, ptr, i64, ptr],
+        "muon_balance_step": [ptr, ptr, ctypes.c_int, i64, i64, ctypes.c_float, ptr],
+    }.items():
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_int
+    lib.muon_ckpt_wgrad_workspace_size.argtypes = [ctypes.POINTER(MuonWgrad)]
+    lib.muon_ckpt_wgrad_workspace_size.restype = ctypes.c_size_t
+    lib.muon_route_workspace_size.argtypes = [ctypes.POINTER(MuonRouting)]
+    lib.muon_route_workspace_size.restype = ctypes.c_size_t
     lib.muon_status_string.argtypes = [ctypes.c_int]
     lib.muon_status_string.restype = ctypes.c_char_p
     lib.muon_last_error.argtypes = []

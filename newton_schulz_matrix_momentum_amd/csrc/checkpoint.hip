@@ -1,0 +1,154 @@
+// 8-bit activation checkpoints: pack, unpack, and SwiGLU forward and backward
+// through them.
+//
+// Every kernel is a pass over rows x cols with a few bytes and a few tens of
+// operations per value, so HBM bounds it.  A thread takes 8 consecutive
+// columns (16 bytes of a 16-bit type, 8 bytes of codes); the 4 neighbouring
+// lanes that share a block of 32 exchange their maxima with two cross-lane
+// moves, so a block's exponent costs no LDS and no second pass.
+#include "ckpt_code.h"
+
+namespace muon {
+namespace {
+
+// max over the 4 lanes of a quad
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));   // lanes 1 0 3 2
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));   // lanes 2 3 0 1
+}
+
+__device__ __forceinline__ uint32_t max_bits(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
+struct Unit {
+  int64_t row;
+  int64_t col;
+  int n;          // columns of the unit inside the row, <= 0: none
+};
+
+__device__ __forceinline__ Unit unit_at(const CkptArgs &args, uint32_t u) {
+  const uint32_t row = (__umulhi(args.per_row.mul, u) + u) >> args.per_row.shift;
+  Unit x;
+  x.row = row;
+  x.col = (int64_t)(u - row * args.per_row.d) * kCkptVec;
+  const int64_t left = args.cols - x.col;
+  x.n = left < kCkptVec ? (int)left : kCkptVec;
+  return x;
+}
+
+// Store a unit's codes and, once per block, its exponent byte.  A unit past
+// cols but inside the 16-byte filling writes zeros (its values are zero).
+template <int FMT>
+__device__ __forceinline__ void put_codes(const CkptMat &m, const Unit &x, int64_t cols, const float (&v)[8], uint32_t b) {
+  if (x.col < ((cols + 15) & ~(int64_t)15)) *(uint2 *)(m.codes + x.row * m.codes_ld + x.col) = encode8<FMT>(v, b);
+  if ((x.col & (kCkptBlock - 1)) == 0) m.scales[x.row * m.scales_ld + x.col / kCkptBlock] = (uint8_t)b;
+}
+
+template <int FMT>
+__device__ __forceinline__ void get_values(const CkptMat &m, const Unit &x, float (&v)[8]) {
+  const uint2 w = *(const uint2 *)(m.codes + x.row * m.codes_ld + x.col);
+  decode8<FMT>(w, m.scales[x.row * m.scales_ld + x.col / kCkptBlock], v);
+}
+
+template <int DT, int FMT>
+__global__ __launch_bounds__(kCkptThreads) void ckpt_pack_kernel(CkptArgs args) {
+  typedef typename Val<DT>::type T;
+  const uint32_t u = blockIdx.x * kCkptThreads + threadIdx.x;
+  if (u >= args.units) return;      // units come in fours: a quad is in or out together
+  const Unit x = unit_at(args, u);
+  float v[8] = {};
+  if (x.n > 0) load8<DT>((const T *)args.a + x.row * args.ld_a + x.col, x.n, v);
+  const uint32_t b = exponent_byte<FMT>(quad_max(max_bits(v)));
+  put_codes<FMT>(args.m[0], x, args.cols, v, b);
+}
+
+template <int DT, int FMT>
+__global__ __launch_bounds__(kCkptThreads) void ckpt_unpack_kernel(CkptArgs args) {
+  typedef typename Val<DT>::type T;
+  const uint32_t u = blockIdx.x * kCkptThreads + threadIdx.x;
+  if (u >= args.units) return;
+  const Unit x = unit_at(args, u);
+  if (x.n <= 0) return;
+  float v[8];
+  get_values<FMT>(args.m[0], x, v);
+  if constexpr (DT == kF16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = saturate_f16(v[i]);
+  }
+  store8<DT>((T *)args.out + x.row * args.ld_out + x.col, x.n, v);
+}
+
+__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+
+template <int DT, int FMT>
+__global__ __launch_bounds__(kCkptThreads) void ckpt_swiglu_kernel(CkptArgs args) {
+  typedef typename Val<DT>::type T;
+  const uint32_t i = blockIdx.x * kCkptThreads + threadIdx.x;
+  if (i >= args.units) return;
+  const Unit x = unit_at(args, i);
+  float g[8] = {}, u[8] = {};
+  if (x.n > 0) {
+    load8<DT>((const T *)args.a + x.row * args.ld_a + x.col, x.n, g);
+    load8<DT>((const T *)args.b + x.row * args.ld_b + x.col, x.n, u);
+  }
+  const uint32_t bg = exponent_byte<FMT>(quad_max(max_bits(g))), bu = exponent_byte<FMT>(quad_max(max_bits(u)));
+  put_codes<FMT>(args.m[0], x, args.cols, g, bg);
+  put_codes<FMT>(args.m[1], x, args.cols, u, bu);
+  if (x.n <= 0) return;
+  float h[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) h[k] = g[k] * sigmoid(g[k]) * u[k];
+  store8<DT>((T *)args.out + x.row * args.ld_out + x.col, x.n, h);
+}
+
+template <int DT, int FMT>
+__global__ __launch_bounds__(kCkptThreads) void ckpt_swiglu_backward_kernel(CkptArgs args) {
+  typedef typename Val<DT>::type T;
+  const uint32_t i = blockIdx.x * kCkptThreads + threadIdx.x;
+  if (i >= args.units) return;
+  const Unit x = unit_at(args, i);
+  if (x.n <= 0) return;
+  float d[8], g[8], u[8], dg[8], du[8], h[8];
+  load8<DT>((const T *)args.a + x.row * args.ld_a + x.col, x.n, d);
+  get_values<FMT>(args.m[0], x, g);
+  get_values<FMT>(args.m[1], x, u);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float s = sigmoid(g[k]);
+    const float gs = g[k] * s;
+    dg[k] = d[k] * u[k] * s * (1.0f + g[k] * (1.0f - s));
+    du[k] = d[k] * gs;
+    h[k] = gs * u[k];
+  }
+  store8<DT>((T *)args.out_g + x.row * args.ld_g + x.col, x.n, dg);
+  store8<DT>((T *)args.out_u + x.row * args.ld_u + x.col, x.n, du);
+  if (args.out) store8<DT>((T *)args.out + x.row * args.ld_out + x.col, x.n, h);
+}
+
+}  // namespace
+
+#define MUON_CKPT_LAUNCH(NAME)                                                                                  \
+  hipError_t launch_##NAME(const CkptArgs &args, int dtype, int format, hipStream_t s) {                        \
+    const dim3 g((args.units + kCkptThreads - 1) / kCkptThreads), b(kCkptThreads);                              \
+    switch (dtype * 2 + format) {                                                                               \
+      case kF32 * 2 + MUON_E4M3: hipLaunchKernelGGL((NAME##_kernel<kF32, MUON_E4M3>), g, b, 0, s, args); break;    \
+      case kF32 * 2 + MUON_INT8: hipLaunchKernelGGL((NAME##_kernel<kF32, MUON_INT8>), g, b, 0, s, args); break;    \
+      case kF16 * 2 + MUON_E4M3: hipLaunchKernelGGL((NAME##_kernel<kF16, MUON_E4M3>), g, b, 0, s, args); break;    \
+      case kF16 * 2 + MUON_INT8: hipLaunchKernelGGL((NAME##_kernel<kF16, MUON_INT8>), g, b, 0, s, args); break;    \
+      case kBF16 * 2 + MUON_E4M3: hipLaunchKernelGGL((NAME##_kernel<kBF16, MUON_E4M3>), g, b, 0, s, args); break;  \
+      case kBF16 * 2 + MUON_INT8: hipLaunchKernelGGL((NAME##_kernel<kBF16, MUON_INT8>), g, b, 0, s, args); break;  \
+      default: return hipErrorInvalidValue;                                                                     \
+    }                                                                                                           \
+    return hipGetLastError();                                                                                   \
+  }
+
+MUON_CKPT_LAUNCH(ckpt_pack)
+MUON_CKPT_LAUNCH(ckpt_unpack)
+MUON_CKPT_LAUNCH(ckpt_swiglu)
+MUON_CKPT_LAUNCH(ckpt_swiglu_backward)
+
+}  // namespace muon

@@ -1,0 +1,157 @@
+// The 8-bit checkpoint's codes on the device: exponent bytes, encoding and
+// decoding of 8 consecutive columns (the format is stated in muon.h).
+#pragma once
+
+#include "train_kernels.h"
+
+namespace muon {
+
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));   // 16 bytes at any 2-byte address
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f32x2v __attribute__((ext_vector_type(2)));
+
+template <int DT> struct Val;
+template <> struct Val<kF32> {
+  typedef float type;
+  static __device__ __forceinline__ float to(float v) { return v; }
+  static __device__ __forceinline__ float from(float v) { return v; }
+};
+template <> struct Val<kBF16> {
+  typedef __bf16 type;
+  static __device__ __forceinline__ float to(__bf16 v) { return (float)v; }
+  static __device__ __forceinline__ __bf16 from(float v) { return (__bf16)v; }
+};
+template <> struct Val<kF16> {
+  typedef _Float16 type;
+  static __device__ __forceinline__ float to(_Float16 v) { return (float)v; }
+  static __device__ __forceinline__ _Float16 from(float v) { return (_Float16)v; }
+};
+
+// p[0 .. n) (n <= 8) as fp32, zeros behind
+template <int DT>
+__device__ __forceinline__ void load8(const typename Val<DT>::type *p, int n, float (&v)[8]) {
+  typedef typename Val<DT>::type T;
+  if (n >= 8) {
+    if constexpr (DT == kF32) {
+      const f32x4u a = *(const f32x4u *)p, b = *(const f32x4u *)(p + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+    } else {
+      const u32x4u a = *(const u32x4u *)p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = Val<DT>::to(__builtin_bit_cast(T, (uint16_t)(a[i] & 0xFFFFu)));
+        v[2 * i + 1] = Val<DT>::to(__builtin_bit_cast(T, (uint16_t)(a[i] >> 16)));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? Val<DT>::to(p[i]) : 0.0f;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(typename Val<DT>::type *p, int n, const float (&v)[8]) {
+  if (n >= 8) {
+    if constexpr (DT == kF32) {
+      f32x4u a, b;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = v[i], b[i] = v[4 + i];
+      *(f32x4u *)p = a;
+      *(f32x4u *)(p + 4) = b;
+    } else {
+      u32x4u a;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        a[i] = (uint32_t)__builtin_bit_cast(uint16_t, Val<DT>::from(v[2 * i])) |
+               ((uint32_t)__builtin_bit_cast(uint16_t, Val<DT>::from(v[2 * i + 1])) << 16);
+      *(u32x4u *)p = a;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = Val<DT>::from(v[i]);
+  }
+}
+
+// The exponent byte of a block whose largest magnitude has the bits m (the
+// bits of |x| order like |x|, infinities and NaN above all): the smallest
+// power of two that brings 1.M 2^(E - 127) to at most Q = 1.75 2^8 (e4m3) or
+// 1.984375 2^6 (int8), at least 2^-111 so that every code times it is a
+// normal fp32 and bf16 number, and at most what keeps Q times it finite.
+template <int FMT>
+__device__ __forceinline__ uint32_t exponent_byte(uint32_t m) {
+  constexpr int kQ = FMT == MUON_E4M3 ? 8 : 6;                          // floor(log2 Q)
+  constexpr uint32_t kFrac = FMT == MUON_E4M3 ? 0x600000u : 0x7E0000u;  // Q's fraction
+  if (m >= 0x7F800000u) return 255u;
+  const int b = (int)(m >> 23) - kQ + ((m & 0x7FFFFFu) > kFrac ? 1 : 0);
+  return (uint32_t)min(max(b, 16), 254 - kQ);
+}
+
+// 2^(127 - b), exact for the bytes exponent_byte gives (255: the codes are dropped)
+__device__ __forceinline__ float inverse_scale(uint32_t b) { return __uint_as_float((254u - min(b, 253u)) << 23); }
+
+// 2^(b - 127), NaN for 255
+__device__ __forceinline__ float scale_of(uint32_t b) {
+  const uint32_t bits = b == 0 ? 0x00400000u : b << 23;
+  return __uint_as_float(b == 255 ? 0x7FC00000u : bits);
+}
+
+// Codes of 8 values.  x 2^-e is exact (a power of two), so this is the one
+// rounding: the fp8 conversion's, or that of adding 1.5 2^23, which leaves
+// the whole number in the low byte.  The clamp only acts on values beyond
+// the largest storable one.
+template <int FMT>
+__device__ __forceinline__ uint2 encode8(const float (&v)[8], uint32_t b) {
+  constexpr float kQ = FMT == MUON_E4M3 ? 448.0f : 127.0f;
+  const float inv = inverse_scale(b);
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = __builtin_amdgcn_fmed3f(v[i] * inv, -kQ, kQ);
+  uint2 w;
+  if constexpr (FMT == MUON_E4M3) {
+    int x = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
+    x = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], x, true);
+    int y = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], 0, false);
+    y = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], y, true);
+    w = make_uint2((uint32_t)x, (uint32_t)y);
+  } else {
+    uint32_t q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __float_as_uint(t[i] + 12582912.0f) & 0xFFu;
+    w.x = q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
+    w.y = q[4] | (q[5] << 8) | (q[6] << 16) | (q[7] << 24);
+  }
+  return b == 255 ? make_uint2(0, 0) : w;
+}
+
+template <int FMT>
+__device__ __forceinline__ void decode4(uint32_t w, float scale, float (&v)[4]) {
+  if constexpr (FMT == MUON_E4M3) {
+    const f32x2v a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    v[0] = a.x * scale;
+    v[1] = a.y * scale;
+    v[2] = b.x * scale;
+    v[3] = b.y * scale;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(w >> (8 * i)) * scale;
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ void decode8(uint2 w, uint32_t b, float (&v)[8]) {
+  const float s = scale_of(b);
+  float lo[4], hi[4];
+  decode4<FMT>(w.x, s, lo);
+  decode4<FMT>(w.y, s, hi);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+}
+
+// fp16 operands and outputs: finite values past the range become +-65504
+__device__ __forceinline__ float saturate_f16(float v) {
+  return fabsf(v) > 65504.0f ? copysignf(65504.0f, v) : v;
+}
+
+}  // namespace muon

@@ -1,0 +1,427 @@
+// Host side of the training operators declared in include/muon.h: argument
+// checks, launch shapes and workspace layout.  Every error is found before
+// anything is enqueued.
+#include "train_kernels.h"
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+using namespace muon;
+
+namespace {
+
+muon_status fail(muon_status s, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return record_error(s, buf);
+}
+
+muon_status done() { return record_error(MUON_OK, ""); }
+
+muon_status launched(hipError_t e, const char *what) {
+  return e == hipSuccess ? done() : fail(MUON_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+constexpr int64_t kMaxCols = int64_t(1) << 20;
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+
+int64_t elem_size(muon_dtype t) { return t == MUON_F32 ? 4 : 2; }
+bool known(muon_dtype t) { return t == MUON_F32 || t == MUON_F16 || t == MUON_BF16; }
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// The bytes a matrix covers: `rows` runs of `width` bytes, `pitch` apart.
+struct Span {
+  uintptr_t lo;
+  int64_t rows, width, pitch;
+  bool out;
+  const char *what;
+};
+
+bool meet(const Span &a, const Span &b) {
+  if (a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+  const uintptr_t ah = a.lo + (uintptr_t)((a.rows - 1) * a.pitch + a.width);
+  const uintptr_t bh = b.lo + (uintptr_t)((b.rows - 1) * b.pitch + b.width);
+  if (a.lo >= bh || b.lo >= ah) return false;
+  if (a.pitch == b.pitch && a.pitch > 0) {
+    // rows of equal pitch may interleave: columns [0, a.width) and [d, d + b.width) of one pitch
+    const int64_t d = (int64_t)((b.lo >= a.lo ? b.lo - a.lo : a.pitch - (int64_t)((a.lo - b.lo) % (uintptr_t)a.pitch)) %
+                                (uintptr_t)a.pitch);
+    if (d >= a.width && d + b.width <= a.pitch) return false;
+  }
+  return true;
+}
+
+muon_status check_spans(const Span *s, int n) {
+  for (int i = 0; i < n; ++i)
+    for (int k = i + 1; k < n; ++k)
+      if ((s[i].out || s[k].out) && meet(s[i], s[k]))
+        return fail(MUON_ERR_INVALID_ARG, "buffers overlap: %s and %s", s[i].what, s[k].what);
+  return MUON_OK;
+}
+
+muon_status check_matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, muon_dtype t, const char *what) {
+  if (!p && rows > 0) return fail(MUON_ERR_INVALID_ARG, "%s is NULL", what);
+  if (rows > 1 && ld < cols) return fail(MUON_ERR_INVALID_ARG, "%s: row stride %lld is below its %lld columns", what, (long long)ld, (long long)cols);
+  if (((uintptr_t)p) & (uintptr_t)(elem_size(t) - 1)) return fail(MUON_ERR_INVALID_ARG, "%s is not aligned to its elements", what);
+  return MUON_OK;
+}
+
+Span span(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t es, bool out, const char *what) {
+  return Span{(uintptr_t)p, rows, cols * es, ld * es, out, what};
+}
+
+int64_t ckpt_blocks(int64_t cols) { return (cols + kCkptBlock - 1) / kCkptBlock; }
+
+muon_status check_ckpt(const muon_ckpt *c, const char *what) {
+  if (!c) return fail(MUON_ERR_INVALID_ARG, "%s is NULL", what);
+  if (c->rows < 0 || c->cols < 1) return fail(MUON_ERR_INVALID_ARG, "%s: rows must be >= 0 and cols >= 1", what);
+  if (c->format != MUON_E4M3 && c->format != MUON_INT8) return fail(MUON_ERR_UNSUPPORTED, "%s: unknown format %d", what, (int)c->format);
+  if (c->cols > kMaxCols || c->rows > kMaxRows || c->rows * ckpt_blocks(c->cols) > (int64_t(1) << 29) - 1)
+    return fail(MUON_ERR_UNSUPPORTED, "%s: %lld x %lld exceeds the supported size", what, (long long)c->rows, (long long)c->cols);
+  if (c->rows > 0 && (!c->codes || !c->scales)) return fail(MUON_ERR_INVALID_ARG, "%s: codes and scales must be non-NULL", what);
+  if ((((uintptr_t)c->codes) & 15) || (c->codes_ld & 15) || c->codes_ld < c->cols)
+    return fail(MUON_ERR_INVALID_ARG, "%s: codes need a 16-byte aligned base and a row stride that is a multiple of 16 and at least cols", what);
+  if (c->scales_ld < ckpt_blocks(c->cols)) return fail(MUON_ERR_INVALID_ARG, "%s: scales_ld is below the blocks of a row", what);
+  return MUON_OK;
+}
+
+Span codes_span(const muon_ckpt *c, bool out, const char *what) {
+  return Span{(uintptr_t)c->codes, c->rows, (c->cols + 15) & ~int64_t(15), c->codes_ld, out, what};
+}
+Span scales_span(const muon_ckpt *c, bool out, const char *what) {
+  return Span{(uintptr_t)c->scales, c->rows, ckpt_blocks(c->cols), c->scales_ld, out, what};
+}
+
+CkptArgs ckpt_args(const muon_ckpt *a, const muon_ckpt *b) {
+  CkptArgs x;
+  std::memset(&x, 0, sizeof(x));
+  x.cols = a->cols;
+  x.m[0] = CkptMat{a->codes, a->scales, a->codes_ld, a->scales_ld};
+  if (b) x.m[1] = CkptMat{b->codes, b->scales, b->codes_ld, b->scales_ld};
+  const int64_t per_row = ckpt_blocks(a->cols) * kCkptLanes;
+  x.per_row = make_fastdiv((uint32_t)per_row);
+  x.units = (uint32_t)(a->rows * per_row);
+  return x;
+}
+
+#define TRY(expr)                      \
+  do {                                 \
+    const muon_status st_ = (expr);    \
+    if (st_ != MUON_OK) return st_;    \
+  } while (0)
+
+muon_status check_pair(const muon_ckpt *a, const muon_ckpt *b) {
+  TRY(check_ckpt(a, "gate_ckpt"));
+  TRY(check_ckpt(b, "up_ckpt"));
+  if (a->rows != b->rows || a->cols != b->cols || a->format != b->format)
+    return fail(MUON_ERR_INVALID_ARG, "gate_ckpt and up_ckpt differ in rows, cols or format");
+  return MUON_OK;
+}
+
+// ------------------------------------------------------------------ wgrad
+
+struct WgradPlan {
+  int splits = 1;
+  int64_t split_len = 0;
+  size_t bytes = 256;
+};
+
+muon_status check_wgrad(const muon_wgrad *a) {
+  if (!a) return fail(MUON_ERR_INVALID_ARG, "args is NULL");
+  if (a->dtype != MUON_F16 && a->dtype != MUON_BF16)
+    return fail(MUON_ERR_UNSUPPORTED, "grad_y must be F16 or BF16 (the matrix operands are 16-bit), got dtype %d", (int)a->dtype);
+  if (!known(a->out_dtype)) return fail(MUON_ERR_UNSUPPORTED, "unknown out_dtype %d", (int)a->out_dtype);
+  TRY(check_ckpt(&a->ckpt, "ckpt"));
+  if (a->slots < 0 || a->outs < 1 || a->experts < 1) return fail(MUON_ERR_INVALID_ARG, "slots must be >= 0, outs and experts >= 1");
+  if (a->slots > kMaxRows || a->outs > kMaxCols || a->outs * a->ckpt.cols > kMaxRows || a->experts > 65535)
+    return fail(MUON_ERR_UNSUPPORTED, "%lld slots, %d matrices of %lld x %lld exceed the supported size", (long long)a->slots, (int)a->experts,
+                (long long)a->outs, (long long)a->ckpt.cols);
+  if (!a->offsets && a->experts != 1) return fail(MUON_ERR_INVALID_ARG, "experts > 1 needs offsets");
+  if (!a->rows_of && a->slots != a->ckpt.rows)
+    return fail(MUON_ERR_INVALID_ARG, "%lld slots for a checkpoint of %lld rows need rows_of", (long long)a->slots, (long long)a->ckpt.rows);
+  return MUON_OK;
+}
+
+// A single matrix of few output tiles has its token range cut into parts
+// that are joined in order afterwards, so that the parts' blocks fill the chip.
+WgradPlan plan_wgrad(const muon_wgrad *a) {
+  WgradPlan p;
+  const int64_t tiles = ((a->outs + kWgradTile - 1) / kWgradTile) * ((a->ckpt.cols + kWgradTile - 1) / kWgradTile);
+  if (a->offsets || a->slots == 0) return p;
+  const int64_t want = std::min<int64_t>((512 + tiles - 1) / tiles, a->slots / 256);
+  if (want <= 1) return p;
+  const int64_t len = ((a->slots + want - 1) / want + kWgradK - 1) / kWgradK * kWgradK;
+  p.splits = (int)((a->slots + len - 1) / len);
+  p.split_len = len;
+  if (p.splits > 1) p.bytes = align256((size_t)p.splits * (size_t)(a->outs * a->ckpt.cols) * 4);
+  return p;
+}
+
+// ---------------------------------------------------------------- routing
+
+muon_status check_routing(const muon_routing *a) {
+  if (!a) return fail(MUON_ERR_INVALID_ARG, "args is NULL");
+  if (!known(a->dtype)) return fail(MUON_ERR_UNSUPPORTED, "unknown dtype %d", (int)a->dtype);
+  if (a->score != MUON_SOFTMAX && a->score != MUON_SIGMOID) return fail(MUON_ERR_INVALID_ARG, "unknown score %d", (int)a->score);
+  if (a->tokens < 0 || a->experts < 1 || a->top_k < 1) return fail(MUON_ERR_INVALID_ARG, "tokens must be >= 0, experts and top_k >= 1");
+  if (a->experts > kRouteMaxExperts || a->top_k > kRouteMaxTopK)
+    return fail(MUON_ERR_UNSUPPORTED, "%d experts, top_k %d: at most %d and %d", (int)a->experts, (int)a->top_k, kRouteMaxExperts, kRouteMaxTopK);
+  if (a->top_k > a->experts) return fail(MUON_ERR_INVALID_ARG, "top_k %d exceeds %d experts", (int)a->top_k, (int)a->experts);
+  if (a->tokens > kMaxRows / a->top_k) return fail(MUON_ERR_UNSUPPORTED, "tokens * top_k must stay below 2^31");
+  if (!std::isfinite(a->scale)) return fail(MUON_ERR_INVALID_ARG, "scale is not finite");
+  return check_matrix(a->logits, a->tokens, a->experts, a->ld_logits, a->dtype, "logits");
+}
+
+muon_status check_groups(const muon_routing *a) {
+  if (a->groups < 1 || a->experts % a->groups != 0) return fail(MUON_ERR_INVALID_ARG, "groups must divide experts");
+  if (a->top_groups < 1 || a->top_groups > a->groups) return fail(MUON_ERR_INVALID_ARG, "top_groups must lie in [1, groups]");
+  if (a->group_top != 1 && a->group_top != 2) return fail(MUON_ERR_INVALID_ARG, "group_top must be 1 or 2");
+  if (a->top_groups < a->groups && a->groups > kRouteMaxGroups)
+    return fail(MUON_ERR_UNSUPPORTED, "at most %d groups", kRouteMaxGroups);
+  if (a->top_k > a->top_groups * (a->experts / a->groups))
+    return fail(MUON_ERR_INVALID_ARG, "top_k %d exceeds the experts of %d groups", (int)a->top_k, (int)a->top_groups);
+  const int lists = !!a->counts + !!a->offsets + !!a->order + !!a->rows;
+  // order and rows of an empty batch have no storage
+  const bool empty = a->tokens == 0 && a->counts && a->offsets;
+  if (lists != 0 && lists != 4 && !empty) return fail(MUON_ERR_INVALID_ARG, "counts, offsets, order and rows are given together or not at all");
+  if (a->load && lists == 0) return fail(MUON_ERR_INVALID_ARG, "load needs the dispatch lists");
+  if (a->load && (((uintptr_t)a->load) & 7)) return fail(MUON_ERR_INVALID_ARG, "load is not aligned to its elements");
+  if (a->tokens > 0 && (!a->expert_ids || !a->weights)) return fail(MUON_ERR_INVALID_ARG, "expert_ids and weights must be non-NULL");
+  return MUON_OK;
+}
+
+int64_t route_blocks(const muon_routing *a) { return (a->tokens + kRouteRows - 1) / kRouteRows; }
+
+size_t route_bytes(const muon_routing *a) {
+  if (!a->counts) return 256;
+  return align256((size_t)(route_blocks(a) * a->experts) * 4) + align256((size_t)(a->tokens * a->top_k) * 4) + 256;
+}
+
+RouteArgs route_args(const muon_routing *a) {
+  RouteArgs x;
+  std::memset(&x, 0, sizeof(x));
+  x.logits = a->logits;
+  x.ld = a->ld_logits;
+  x.tokens = a->tokens;
+  x.bias = a->bias;
+  x.token_mask = a->token_mask;
+  x.ids = a->expert_ids;
+  x.weights = a->weights;
+  x.experts = a->experts;
+  x.top_k = a->top_k;
+  x.groups = a->groups;
+  x.top_groups = a->top_groups;
+  x.group_top = a->group_top;
+  x.sigmoid = a->score == MUON_SIGMOID;
+  x.renormalize = a->renormalize != 0;
+  x.scale = a->scale;
+  x.blocks = (int32_t)route_blocks(a);
+  return x;
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status muon_ckpt_pack(const void *x, int64_t ld, muon_dtype dtype, const muon_ckpt *ckpt, void *stream) {
+  if (!known(dtype)) return fail(MUON_ERR_UNSUPPORTED, "unknown dtype %d", (int)dtype);
+  TRY(check_ckpt(ckpt, "ckpt"));
+  TRY(check_matrix(x, ckpt->rows, ckpt->cols, ld, dtype, "x"));
+  const Span s[] = {span(x, ckpt->rows, ckpt->cols, ld, elem_size(dtype), false, "x"), codes_span(ckpt, true, "codes"),
+                    scales_span(ckpt, true, "scales")};
+  TRY(check_spans(s, 3));
+  if (ckpt->rows == 0) return done();
+  CkptArgs a = ckpt_args(ckpt, nullptr);
+  a.a = x;
+  a.ld_a = ld;
+  return launched(launch_ckpt_pack(a, (int)dtype, (int)ckpt->format, (hipStream_t)stream), "muon_ckpt_pack");
+}
+
+muon_status muon_ckpt_unpack(const muon_ckpt *ckpt, void *x, int64_t ld, muon_dtype dtype, void *stream) {
+  if (!known(dtype)) return fail(MUON_ERR_UNSUPPORTED, "unknown dtype %d", (int)dtype);
+  TRY(check_ckpt(ckpt, "ckpt"));
+  TRY(check_matrix(x, ckpt->rows, ckpt->cols, ld, dtype, "x"));
+  const Span s[] = {span(x, ckpt->rows, ckpt->cols, ld, elem_size(dtype), true, "x"), codes_span(ckpt, false, "codes"),
+                    scales_span(ckpt, false, "scales")};
+  TRY(check_spans(s, 3));
+  if (ckpt->rows == 0) return done();
+  CkptArgs a = ckpt_args(ckpt, nullptr);
+  a.out = x;
+  a.ld_out = ld;
+  return launched(launch_ckpt_unpack(a, (int)dtype, (int)ckpt->format, (hipStream_t)stream), "muon_ckpt_unpack");
+}
+
+muon_status muon_ckpt_swiglu(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, muon_dtype dtype, void *h, int64_t ld_h,
+                             const muon_ckpt *gate_ckpt, const muon_ckpt *up_ckpt, void *stream) {
+  if (!known(dtype)) return fail(MUON_ERR_UNSUPPORTED, "unknown dtype %d", (int)dtype);
+  TRY(check_pair(gate_ckpt, up_ckpt));
+  const int64_t rows = gate_ckpt->rows, cols = gate_ckpt->cols, es = elem_size(dtype);
+  TRY(check_matrix(gate, rows, cols, ld_gate, dtype, "gate"));
+  TRY(check_matrix(up, rows, cols, ld_up, dtype, "up"));
+  TRY(check_matrix(h, rows, cols, ld_h, dtype, "h"));
+  const Span s[] = {span(gate, rows, cols, ld_gate, es, false, "gate"), span(up, rows, cols, ld_up, es, false, "up"),
+                    span(h, rows, cols, ld_h, es, true, "h"), codes_span(gate_ckpt, true, "gate codes"),
+                    scales_span(gate_ckpt, true, "gate scales"), codes_span(up_ckpt, true, "up codes"),
+                    scales_span(up_ckpt, true, "up scales")};
+  TRY(check_spans(s, 7));
+  if (rows == 0) return done();
+  CkptArgs a = ckpt_args(gate_ckpt, up_ckpt);
+  a.a = gate;
+  a.ld_a = ld_gate;
+  a.b = up;
+  a.ld_b = ld_up;
+  a.out = h;
+  a.ld_out = ld_h;
+  return launched(launch_ckpt_swiglu(a, (int)dtype, (int)gate_ckpt->format, (hipStream_t)stream), "muon_ckpt_swiglu");
+}
+
+muon_status muon_ckpt_swiglu_backward(const void *grad_h, int64_t ld_grad_h, muon_dtype dtype, const muon_ckpt *gate_ckpt,
+                                      const muon_ckpt *up_ckpt, void *grad_gate, int64_t ld_grad_gate, void *grad_up, int64_t ld_grad_up,
+                                      void *h, int64_t ld_h, void *stream) {
+  if (!known(dtype)) return fail(MUON_ERR_UNSUPPORTED, "unknown dtype %d", (int)dtype);
+  TRY(check_pair(gate_ckpt, up_ckpt));
+  const int64_t rows = gate_ckpt->rows, cols = gate_ckpt->cols, es = elem_size(dtype);
+  TRY(check_matrix(grad_h, rows, cols, ld_grad_h, dtype, "grad_h"));
+  TRY(check_matrix(grad_gate, rows, cols, ld_grad_gate, dtype, "grad_gate"));
+  TRY(check_matrix(grad_up, rows, cols, ld_grad_up, dtype, "grad_up"));
+  if (h) TRY(check_matrix(h, rows, cols, ld_h, dtype, "h"));
+  const Span s[] = {span(grad_h, rows, cols, ld_grad_h, es, false, "grad_h"), span(grad_gate, rows, cols, ld_grad_gate, es, true, "grad_gate"),
+                    span(grad_up, rows, cols, ld_grad_up, es, true, "grad_up"), codes_span(gate_ckpt, false, "gate codes"),
+                    scales_span(gate_ckpt, false, "gate scales"), codes_span(up_ckpt, false, "up codes"),
+                    scales_span(up_ckpt, false, "up scales"), span(h, h ? rows : 0, cols, ld_h, es, true, "h")};
+  TRY(check_spans(s, 8));
+  if (rows == 0) return done();
+  CkptArgs a = ckpt_args(gate_ckpt, up_ckpt);
+  a.a = grad_h;
+  a.ld_a = ld_grad_h;
+  a.out_g = grad_gate;
+  a.ld_g = ld_grad_gate;
+  a.out_u = grad_up;
+  a.ld_u = ld_grad_up;
+  a.out = h;
+  a.ld_out = ld_h;
+  return launched(launch_ckpt_swiglu_backward(a, (int)dtype, (int)gate_ckpt->format, (hipStream_t)stream), "muon_ckpt_swiglu_backward");
+}
+
+size_t muon_ckpt_wgrad_workspace_size(const muon_wgrad *args) {
+  if (check_wgrad(args) != MUON_OK) return 0;
+  return plan_wgrad(args).bytes;
+}
+
+muon_status muon_ckpt_wgrad(const muon_wgrad *args, void *workspace, size_t workspace_bytes, void *stream) {
+  TRY(check_wgrad(args));
+  const muon_wgrad &w = *args;
+  TRY(check_matrix(w.grad_y, w.slots, w.outs, w.ld_grad_y, w.dtype, "grad_y"));
+  TRY(check_matrix(w.out, 1, w.outs, w.outs, w.out_dtype, "out"));
+  const WgradPlan p = plan_wgrad(args);
+  if (!workspace || (((uintptr_t)workspace) & 255)) return fail(MUON_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
+  if (workspace_bytes < p.bytes)
+    return fail(MUON_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", workspace_bytes, p.bytes);
+  const int64_t size = w.outs * w.ckpt.cols;
+  const Span s[] = {span(w.grad_y, w.slots, w.outs, w.ld_grad_y, 2, false, "grad_y"), codes_span(&w.ckpt, false, "codes"),
+                    scales_span(&w.ckpt, false, "scales"), span(w.offsets, w.offsets ? 1 : 0, (int64_t)w.experts + 1, 0, 4, false, "offsets"),
+                    span(w.rows_of, w.rows_of ? 1 : 0, w.slots, 0, 4, false, "rows_of"),
+                    span(w.out, w.experts, size, size, elem_size(w.out_dtype), true, "out"),
+                    span(workspace, 1, (int64_t)p.bytes, 0, 1, true, "workspace")};
+  TRY(check_spans(s, 7));
+  WgradArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.dy = w.grad_y;
+  a.codes = w.ckpt.codes;
+  a.scales = w.ckpt.scales;
+  a.offsets = w.offsets;
+  a.rows_of = w.rows_of;
+  a.out = w.out;
+  a.part = (float *)workspace;
+  a.ld_dy = w.ld_grad_y;
+  a.codes_ld = w.ckpt.codes_ld;
+  a.scales_ld = w.ckpt.scales_ld;
+  a.slots = w.slots;
+  a.ckpt_rows = w.ckpt.rows;
+  a.outs = (int32_t)w.outs;
+  a.cols = (int32_t)w.ckpt.cols;
+  a.experts = w.experts;
+  a.splits = p.splits;
+  a.split_len = p.split_len;
+  a.tiles_n = (int32_t)((w.outs + kWgradTile - 1) / kWgradTile);
+  a.tiles_d = (int32_t)((w.ckpt.cols + kWgradTile - 1) / kWgradTile);
+  a.out_dtype = (int32_t)w.out_dtype;
+  a.accumulate = w.accumulate != 0;
+  a.transposed = w.transposed != 0;
+  hipError_t e = launch_wgrad(a, (int)w.dtype, (int)w.ckpt.format, (hipStream_t)stream);
+  if (e == hipSuccess && p.splits > 1) e = launch_wgrad_join(a, (hipStream_t)stream);
+  return launched(e, "muon_ckpt_wgrad");
+}
+
+size_t muon_route_workspace_size(const muon_routing *args) {
+  if (check_routing(args) != MUON_OK || check_groups(args) != MUON_OK) return 0;
+  return route_bytes(args);
+}
+
+muon_status muon_route(const muon_routing *args, void *workspace, size_t workspace_bytes, void *stream) {
+  TRY(check_routing(args));
+  TRY(check_groups(args));
+  const size_t need = route_bytes(args);
+  if (!workspace || (((uintptr_t)workspace) & 255)) return fail(MUON_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
+  if (workspace_bytes < need) return fail(MUON_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  const int64_t E = args->experts, T = args->tokens, K = args->top_k;
+  auto list = [](const void *p, int64_t n, int64_t es, bool out, const char *what) { return span(p, p && n > 0 ? 1 : 0, n, 0, es, out, what); };
+  const Span s[] = {span(args->logits, T, E, args->ld_logits, elem_size(args->dtype), false, "logits"),
+                    list(args->bias, E, 4, false, "bias"), list(args->token_mask, T, 1, false, "token_mask"),
+                    list(args->expert_ids, T * K, 4, true, "expert_ids"), list(args->weights, T * K, 4, true, "weights"),
+                    list(args->counts, E, 4, true, "counts"), list(args->offsets, E + 1, 4, true, "offsets"),
+                    list(args->order, T * K, 4, true, "order"), list(args->rows, T * K, 4, true, "rows"),
+                    list(args->load, E, 8, true, "load"), list(workspace, (int64_t)need, 1, true, "workspace")};
+  TRY(check_spans(s, 11));
+  const bool lists = args->counts != nullptr;
+  if (T == 0 && !lists) return done();
+  RouteArgs a = route_args(args);
+  a.counts = args->counts;
+  a.offsets = args->offsets;
+  a.order = args->order;
+  a.rows = args->rows;
+  a.load = args->load;
+  a.lists = lists;
+  a.hist = (int32_t *)workspace;
+  a.rank = (int32_t *)((char *)workspace + align256((size_t)(route_blocks(args) * E) * 4));
+  return launched(launch_route(a, (int)args->dtype, (hipStream_t)stream), "muon_route");
+}
+
+muon_status muon_route_backward(const muon_routing *args, const float *grad_weights, void *grad_logits, int64_t ld_grad_logits, void *stream) {
+  TRY(check_routing(args));
+  const int64_t E = args->experts, T = args->tokens, K = args->top_k;
+  TRY(check_matrix(grad_logits, T, E, ld_grad_logits, args->dtype, "grad_logits"));
+  if (T == 0) return done();
+  if (!args->expert_ids || !grad_weights) return fail(MUON_ERR_INVALID_ARG, "expert_ids and grad_weights must be non-NULL");
+  const int64_t es = elem_size(args->dtype);
+  const Span s[] = {span(args->logits, T, E, args->ld_logits, es, false, "logits"), span(args->expert_ids, 1, T * K, 0, 4, false, "expert_ids"),
+                    span(grad_weights, 1, T * K, 0, 4, false, "grad_weights"), span(grad_logits, T, E, ld_grad_logits, es, true, "grad_logits")};
+  TRY(check_spans(s, 4));
+  RouteArgs a = route_args(args);
+  a.grad_weights = grad_weights;
+  a.grad_logits = grad_logits;
+  a.ld_grad = ld_grad_logits;
+  return launched(launch_route_backward(a, (int)args->dtype, (hipStream_t)stream), "muon_route_backward");
+}
+
+muon_status muon_balance_step(float *bias, const void *counts, int count_bytes, int64_t layers, int64_t experts, float rate, void *stream) {
+  if (layers < 0 || experts < 1) return fail(MUON_ERR_INVALID_ARG, "layers must be >= 0 and experts >= 1");
+  if (count_bytes != 4 && count_bytes != 8) return fail(MUON_ERR_UNSUPPORTED, "counts are int32 (4) or int64 (8), got %d bytes", count_bytes);
+  if (!std::isfinite(rate)) return fail(MUON_ERR_INVALID_ARG, "rate is not finite");
+  if (layers > kMaxRows || experts > kMaxCols) return fail(MUON_ERR_UNSUPPORTED, "%lld x %lld exceeds the supported size", (long long)layers, (long long)experts);
+  if (layers == 0) return done();
+  if (!bias || !counts) return fail(MUON_ERR_INVALID_ARG, "bias and counts must be non-NULL");
+  if ((((uintptr_t)counts) & (uintptr_t)(count_bytes - 1)) || (((uintptr_t)bias) & 3))
+    return fail(MUON_ERR_INVALID_ARG, "bias and counts must be aligned to their elements");
+  const Span s[] = {span(bias, 1, layers * experts, 0, 4, true, "bias"), span(counts, 1, layers * experts, 0, count_bytes, false, "counts")};
+  TRY(check_spans(s, 2));
+  return launched(launch_balance(bias, counts, count_bytes, layers, (int)experts, rate, (hipStream_t)stream), "muon_balance_step");
+}
+
+}  // extern "C"

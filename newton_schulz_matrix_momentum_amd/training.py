@@ -1,0 +1,377 @@
+"""Training operators around the optimizer step, over torch tensors.
+
+8-bit activation checkpoints (``checkpoint_pack``, ``checkpoint_unpack``,
+``checkpoint_swiglu`` and its backward pass), the weight gradients that come
+out of them (``checkpoint_wgrad``: what ``muon_step`` takes as ``grad``), and
+routing to experts (``route``, ``route_backward`` and the bias step
+``balance_step``).  The mathematics and the formats are stated in
+include/muon.h.
+
+Every call is enqueued on torch's current stream of the tensors' device and
+returns without synchronising.  Matrices are 2-D GPU tensors with unit column
+stride; rows may be strided (a half of a wider matrix).  Outputs are allocated
+unless given.  Calls are functional (no autograd graph) and can be captured in
+a HIP graph; workspaces come from torch's allocator, so a captured call's
+belongs to its graph.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import _lib
+
+_DT = {torch.float32: _lib.MUON_F32, torch.float16: _lib.MUON_F16, torch.bfloat16: _lib.MUON_BF16}
+_FORMATS = {"e4m3": _lib.MUON_E4M3, "int8": _lib.MUON_INT8}
+_SCORES = {"softmax": _lib.MUON_SOFTMAX, "sigmoid": _lib.MUON_SIGMOID}
+_COUNT_BYTES = {torch.int32: 4, torch.int64: 8}
+BLOCK = _lib.CKPT_BLOCK
+
+
+def _matrix(t, name, shape=None, dtype=None, device=None) -> int:
+    """Checks a matrix with unit column stride; returns its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor (got %s)" % (name, t.device))
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dim() != 2:
+        raise ValueError("%s must be 2-D" % name)
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if dtype is not None:
+        if t.dtype != dtype:
+            raise ValueError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    elif t.dtype not in _DT:
+        raise ValueError("%s must be float32, float16 or bfloat16 (got %s)" % (name, t.dtype))
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have unit column stride" % name)
+    return t.stride(0) if rows > 1 else cols
+
+
+def _flat(t, name, shape, dtype, device) -> int:
+    """Checks a contiguous tensor; returns its address."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _call(device, fn, *args) -> None:
+    """fn(*args, stream) with the tensors' device current."""
+    if device.index == torch.cuda.current_device():
+        _lib.check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+        return
+    with torch.cuda.device(device):
+        _lib.check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def _workspace(workspace, need, device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on %s" % device)
+    # one allocated on another stream stays reserved until this stream is done with it
+    if not torch.cuda.is_current_stream_capturing():
+        workspace.record_stream(torch.cuda.current_stream(device))
+    return workspace
+
+
+def _size(n: int) -> int:
+    if n == 0:
+        raise _lib.MuonError(_lib.MUON_ERR_INVALID_ARG, _lib.last_error())
+    return n
+
+
+class Checkpoint:
+    """An activation of ``rows`` x ``cols`` values kept in 8 bits: ``codes`` (uint8,
+    rows x a multiple of 16 that is at least cols), ``scales`` (uint8, rows x
+    ceil(cols / 32)) and ``format`` ("e4m3" or "int8")."""
+
+    __slots__ = ("codes", "scales", "cols", "format")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, format: str = "e4m3"):
+        if format not in _FORMATS:
+            raise ValueError("format must be one of %s (got %r)" % (sorted(_FORMATS), format))
+        if cols < 1:
+            raise ValueError("cols must be >= 1")
+        ld = _matrix(codes, "codes", None, torch.uint8)
+        rows = codes.shape[0]
+        _matrix(scales, "scales", (rows, -(-cols // BLOCK)), torch.uint8, codes.device)
+        if codes.shape[1] < cols or codes.shape[1] % 16 or ld % 16:
+            raise ValueError("codes must have a multiple of 16 columns, at least cols = %d (got %d)" % (cols, codes.shape[1]))
+        self.codes, self.scales, self.cols, self.format = codes, scales, int(cols), format
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, format: str = "e4m3", device="cuda") -> "Checkpoint":
+        if cols < 1:
+            raise ValueError("cols must be >= 1")
+        return cls(torch.empty(rows, -(-cols // 16) * 16, dtype=torch.uint8, device=device),
+                   torch.empty(rows, -(-cols // BLOCK), dtype=torch.uint8, device=device), cols, format)
+
+    @property
+    def shape(self):
+        return self.codes.shape[0], self.cols
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+    def _record(self) -> "_lib.MuonCkpt":
+        c, s = self.codes, self.scales
+        rows = c.shape[0]
+        return _lib.MuonCkpt(c.data_ptr(), s.data_ptr(), rows, self.cols, c.stride(0) if rows > 1 else c.shape[1],
+                             s.stride(0) if rows > 1 else s.shape[1], _FORMATS[self.format])
+
+
+def _saved(ckpt, name, shape=None, device=None) -> Checkpoint:
+    if not isinstance(ckpt, Checkpoint):
+        raise TypeError("%s must be a Checkpoint" % name)
+    if shape is not None and ckpt.shape != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, ckpt.shape, tuple(shape)))
+    if device is not None and ckpt.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, ckpt.device, device))
+    return ckpt
+
+
+def _output(out, name, shape, dtype, device):
+    """(tensor, row stride) of a matrix output, allocated if None."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device), shape[1]
+    return out, _matrix(out, name, shape, dtype, device)
+
+
+def checkpoint_pack(x: torch.Tensor, *, format: str = "e4m3", out: Optional[Checkpoint] = None) -> Checkpoint:
+    """The 8-bit checkpoint of ``x`` (tokens x cols, float32 / float16 /
+    bfloat16); ``out`` is a checkpoint of x's shape to write instead of a new
+    one (its format then counts)."""
+    ld = _matrix(x, "x")
+    if out is None:
+        out = Checkpoint.empty(x.shape[0], x.shape[1], format, x.device)
+    _saved(out, "out", x.shape, x.device)
+    rec = out._record()
+    _call(x.device, _lib.load().muon_ckpt_pack, x.data_ptr(), ld, _DT[x.dtype], rec)
+    return out
+
+
+def checkpoint_unpack(ckpt: Checkpoint, *, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values a checkpoint stands for, exact in float32 and bfloat16."""
+    _saved(ckpt, "ckpt")
+    if out is not None:
+        dtype = out.dtype
+    if dtype not in _DT:
+        raise ValueError("dtype must be float32, float16 or bfloat16 (got %s)" % dtype)
+    out, ld = _output(out, "out", ckpt.shape, dtype, ckpt.device)
+    _call(ckpt.device, _lib.load().muon_ckpt_unpack, ckpt._record(), out.data_ptr(), ld, _DT[dtype])
+    return out
+
+
+def checkpoint_swiglu(gate: torch.Tensor, up: torch.Tensor, *, format: str = "e4m3", out: Optional[torch.Tensor] = None,
+                      gate_out: Optional[Checkpoint] = None, up_out: Optional[Checkpoint] = None):
+    """``(h, gate checkpoint, up checkpoint)`` with h = gate * sigmoid(gate) * up,
+    in one pass."""
+    ld_g = _matrix(gate, "gate")
+    ld_u = _matrix(up, "up", gate.shape, gate.dtype, gate.device)
+    rows, cols = gate.shape
+    h, ld_h = _output(out, "out", (rows, cols), gate.dtype, gate.device)
+    gate_out = Checkpoint.empty(rows, cols, format, gate.device) if gate_out is None else _saved(gate_out, "gate_out", gate.shape, gate.device)
+    up_out = Checkpoint.empty(rows, cols, format, gate.device) if up_out is None else _saved(up_out, "up_out", gate.shape, gate.device)
+    _call(gate.device, _lib.load().muon_ckpt_swiglu, gate.data_ptr(), ld_g, up.data_ptr(), ld_u, _DT[gate.dtype], h.data_ptr(), ld_h,
+          gate_out._record(), up_out._record())
+    return h, gate_out, up_out
+
+
+def checkpoint_swiglu_backward(grad_h: torch.Tensor, gate: Checkpoint, up: Checkpoint, *, recompute: bool = True,
+                               grad_gate: Optional[torch.Tensor] = None, grad_up: Optional[torch.Tensor] = None,
+                               h: Optional[torch.Tensor] = None):
+    """``(grad_gate, grad_up, h)`` from the two checkpoints; h, the product
+    recomputed from them, is None when ``recompute`` is false and none is given."""
+    ld_d = _matrix(grad_h, "grad_h")
+    device, dtype, shape = grad_h.device, grad_h.dtype, tuple(grad_h.shape)
+    _saved(gate, "gate", shape, device)
+    _saved(up, "up", shape, device)
+    grad_gate, ld_g = _output(grad_gate, "grad_gate", shape, dtype, device)
+    grad_up, ld_u = _output(grad_up, "grad_up", shape, dtype, device)
+    ld_h = shape[1]
+    if recompute or h is not None:
+        h, ld_h = _output(h, "h", shape, dtype, device)
+    _call(device, _lib.load().muon_ckpt_swiglu_backward, grad_h.data_ptr(), ld_d, _DT[dtype], gate._record(), up._record(),
+          grad_gate.data_ptr(), ld_g, grad_up.data_ptr(), ld_u, None if h is None else h.data_ptr(), ld_h)
+    return grad_gate, grad_up, h
+
+
+def checkpoint_wgrad(grad_y: torch.Tensor, ckpt: Checkpoint, *, out: Optional[torch.Tensor] = None,
+                     out_dtype: torch.dtype = torch.float32, transposed: bool = False, accumulate: bool = False,
+                     offsets: Optional[torch.Tensor] = None, rows: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Weight gradient of y = x W^T out of x's checkpoint: dW[n, d] = sum over
+    tokens of grad_y[:, n] * x[:, d], shaped outs x cols, or cols x outs when
+    ``transposed``.  ``grad_y`` is float16 or bfloat16.
+
+    ``offsets`` (int32, experts + 1) makes one matrix for each expert out of its
+    slots offsets[e] .. offsets[e + 1] of grad_y, the result experts x outs x
+    cols; ``rows`` (int32, one a slot) is the checkpoint row of each slot (as
+    ``route`` gives both).  ``accumulate`` adds to ``out``."""
+    ld = _matrix(grad_y, "grad_y")
+    _saved(ckpt, "ckpt", None, grad_y.device)
+    device = grad_y.device
+    slots, outs = grad_y.shape
+    experts = 1
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.numel() < 2:
+            raise ValueError("offsets must hold experts + 1 >= 2 numbers")
+        experts = offsets.numel() - 1
+        _flat(offsets, "offsets", (experts + 1,), torch.int32, device)
+    if rows is not None:
+        _flat(rows, "rows", (slots,), torch.int32, device)
+    shape = (ckpt.cols, outs) if transposed else (outs, ckpt.cols)
+    if offsets is not None:
+        shape = (experts,) + shape
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        if out_dtype not in _DT:
+            raise ValueError("out_dtype must be float32, float16 or bfloat16 (got %s)" % out_dtype)
+        out = torch.empty(shape, dtype=out_dtype, device=device)
+    else:
+        if out.dtype not in _DT:
+            raise ValueError("out must be float32, float16 or bfloat16 (got %s)" % out.dtype)
+        _flat(out, "out", shape, out.dtype, device)
+    args = _lib.MuonWgrad(grad_y.data_ptr(), ld, slots, outs, _DT[grad_y.dtype], ckpt._record(), experts, int(transposed),
+                          None if offsets is None else offsets.data_ptr(), None if rows is None else rows.data_ptr(),
+                          out.data_ptr(), _DT[out.dtype], int(accumulate))
+    lib = _lib.load()
+    ref = ctypes.byref(args)
+    ws = _workspace(workspace, _size(lib.muon_ckpt_wgrad_workspace_size(ref)), device)
+    _call(device, lib.muon_ckpt_wgrad, ref, ws.data_ptr(), ws.numel())
+    return out
+
+
+class Routing(NamedTuple):
+    """What ``route`` gives: ``experts`` (int32) and ``weights`` (float32), tokens x
+    top_k; and the dispatch lists (None when not asked for) ``counts`` and
+    ``offsets`` (experts, experts + 1), ``order`` and ``rows`` (tokens * top_k)."""
+
+    experts: torch.Tensor
+    weights: torch.Tensor
+    counts: Optional[torch.Tensor]
+    offsets: Optional[torch.Tensor]
+    order: Optional[torch.Tensor]
+    rows: Optional[torch.Tensor]
+
+
+def _routing(logits, ld, top_k, score, renormalize, scale):
+    if score not in _SCORES:
+        raise ValueError("score must be one of %s (got %r)" % (sorted(_SCORES), score))
+    a = _lib.MuonRouting()
+    a.logits = logits.data_ptr()
+    a.ld_logits = ld
+    a.tokens, a.experts = logits.shape
+    a.dtype = _DT[logits.dtype]
+    a.top_k = top_k
+    a.score = _SCORES[score]
+    a.groups = a.top_groups = 1
+    a.group_top = 2
+    a.renormalize = int(renormalize)
+    a.scale = scale
+    return a
+
+
+def route(logits: torch.Tensor, top_k: int, *, bias: Optional[torch.Tensor] = None, score: str = "softmax", groups: int = 1,
+          top_groups: int = 1, group_top: int = 2, renormalize: bool = True, scale: float = 1.0,
+          token_mask: Optional[torch.Tensor] = None, dispatch: bool = True, load: Optional[torch.Tensor] = None,
+          workspace: Optional[torch.Tensor] = None) -> Routing:
+    """Routes each token (a row of ``logits``: tokens x experts) to ``top_k`` experts.
+
+    Scores are a softmax or sigmoid; ``bias`` (float32, experts) enters the
+    choice alone; of ``groups`` equal runs of experts the ``top_groups`` best
+    by the sum of their ``group_top`` (1 or 2) best choices stay;
+    weights are the chosen scores, summing to ``scale`` when ``renormalize``.
+    ``token_mask`` (bool or uint8, tokens) is false where a batch is padded.
+    ``dispatch`` asks for the lists by expert; ``load`` (int64, experts) gets
+    the counts added."""
+    ld = _matrix(logits, "logits")
+    device = logits.device
+    tokens, experts = logits.shape
+    top_k = int(top_k)
+    if experts < 1:
+        raise ValueError("logits must have at least one expert")
+    a = _routing(logits, ld, top_k, score, renormalize, scale)
+    a.groups, a.top_groups, a.group_top = groups, top_groups, group_top
+    if bias is not None:
+        a.bias = _flat(bias, "bias", (experts,), torch.float32, device)
+    if token_mask is not None:
+        if token_mask.dtype != torch.bool:
+            _flat(token_mask, "token_mask", (tokens,), torch.uint8, device)
+        a.token_mask = _flat(token_mask, "token_mask", (tokens,), token_mask.dtype, device)
+    if load is not None:
+        a.load = _flat(load, "load", (experts,), torch.int64, device)
+    if top_k < 1:
+        raise ValueError("top_k must be >= 1")
+    ids = torch.empty(tokens, top_k, dtype=torch.int32, device=device)
+    weights = torch.empty(tokens, top_k, dtype=torch.float32, device=device)
+    a.expert_ids, a.weights = ids.data_ptr(), weights.data_ptr()
+    counts = offsets = order = rows = None
+    if dispatch:
+        counts = torch.empty(experts, dtype=torch.int32, device=device)
+        offsets = torch.empty(experts + 1, dtype=torch.int32, device=device)
+        order = torch.empty(tokens * top_k, dtype=torch.int32, device=device)
+        rows = torch.empty(tokens * top_k, dtype=torch.int32, device=device)
+        a.counts, a.offsets, a.order, a.rows = counts.data_ptr(), offsets.data_ptr(), order.data_ptr(), rows.data_ptr()
+    lib = _lib.load()
+    ref = ctypes.byref(a)
+    ws = _workspace(workspace, _size(lib.muon_route_workspace_size(ref)), device)
+    _call(device, lib.muon_route, ref, ws.data_ptr(), ws.numel())
+    return Routing(ids, weights, counts, offsets, order, rows)
+
+
+def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, experts: torch.Tensor, *, score: str = "softmax",
+                   renormalize: bool = True, scale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of ``route``'s weights with respect to ``logits``, in logits' dtype:
+    ``grad_weights`` (float32) and ``experts`` (int32, as ``route`` gave them)
+    are tokens x top_k.  The choice itself carries no gradient."""
+    ld = _matrix(logits, "logits")
+    device = logits.device
+    tokens = logits.shape[0]
+    if not isinstance(experts, torch.Tensor) or experts.dim() != 2:
+        raise ValueError("experts must be a tensor of tokens x top_k")
+    top_k = experts.shape[1]
+    a = _routing(logits, ld, top_k, score, renormalize, scale)
+    a.expert_ids = _flat(experts, "experts", (tokens, top_k), torch.int32, device)
+    dw = _flat(grad_weights, "grad_weights", (tokens, top_k), torch.float32, device)
+    out, ld_out = _output(out, "out", tuple(logits.shape), logits.dtype, device)
+    _call(device, _lib.load().muon_route_backward, ctypes.byref(a), dw, out.data_ptr(), ld_out)
+    return out
+
+
+def balance_step(bias: torch.Tensor, counts: torch.Tensor, *, rate: float) -> None:
+    """bias += rate * sign(mean(counts) - counts) over the last axis, in place:
+    ``bias`` (float32) and ``counts`` (int32 or int64) are experts, or layers x
+    experts."""
+    if not isinstance(bias, torch.Tensor) or not isinstance(counts, torch.Tensor):
+        raise TypeError("bias and counts must be torch.Tensors")
+    if bias.dim() not in (1, 2) or bias.shape[-1] < 1:
+        raise ValueError("bias must be experts, or layers x experts")
+    if not bias.is_cuda:
+        raise ValueError("bias must be a GPU tensor (got %s)" % bias.device)
+    if counts.dtype not in _COUNT_BYTES:
+        raise ValueError("counts must be int32 or int64 (got %s)" % counts.dtype)
+    b = _flat(bias, "bias", tuple(bias.shape), torch.float32, bias.device)
+    c = _flat(counts, "counts", tuple(bias.shape), counts.dtype, bias.device)
+    layers = bias.shape[0] if bias.dim() == 2 else 1
+    _call(bias.device, _lib.load().muon_balance_step, b, c, _COUNT_BYTES[counts.dtype], layers, bias.shape[-1], float(rate))

@@ -1,0 +1,603 @@
+"""The training operators on the GPU against their fp64 definitions.
+
+Tolerances count roundings: a result stored in a type is off by at most half a
+step (eps / 2 relative, half the smallest subnormal near zero), on top of the
+fp32 arithmetic before it, whose bound each test states.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import training_oracle as ref
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+U32 = 2.0 ** -24                                     # half a step of fp32
+
+
+@pytest.fixture(scope="module")
+def nsm():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import newton_schulz_matrix_momentum_amd as m
+    m.load()
+    return m
+
+
+def to64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def half_step(want, dtype):
+    """Half a step of `dtype` around each value."""
+    info = torch.finfo(DT[dtype])
+    return np.abs(want) * info.eps / 2 + info.tiny * info.eps / 2
+
+
+def near(got, want, tol, what):
+    got = to64(got)
+    assert got.shape == want.shape, (what, got.shape, want.shape)
+    bad = np.isnan(want)
+    assert np.array_equal(np.isnan(got), bad), "%s: NaN elsewhere" % what
+    inf = np.isinf(want)
+    assert np.array_equal(got[inf], want[inf]), "%s: infinities differ" % what
+    ok = ~bad & ~inf
+    err = np.abs(got[ok] - want[ok])
+    over = err > np.broadcast_to(tol, want.shape)[ok]
+    assert not over.any(), "%s: %d of %d beyond the bound, worst by %.3g" % (
+        what, over.sum(), over.size, float((err / np.maximum(np.broadcast_to(tol, want.shape)[ok], 1e-300)).max()))
+
+
+def strided(t, ld):
+    """t's values as the left part of a wider matrix whose other columns hold NaN."""
+    wide = torch.full((t.shape[0], ld), math.nan, dtype=t.dtype, device=t.device)
+    wide[:, :t.shape[1]] = t
+    return wide[:, :t.shape[1]]
+
+
+def activations(rows, cols, dtype, seed):
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=gen) * torch.exp(torch.randn(cols, generator=gen))
+    return x.to(DT[dtype])
+
+
+# ---------------------------------------------------------------- checkpoints
+
+SHAPES = [(1, 1), (1, 31), (3, 32), (5, 33), (2, 47), (7, 192), (33, 517), (128, 1024)]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_pack_and_unpack_are_exact(nsm, dtype, fmt):
+    for k, (rows, cols) in enumerate(SHAPES):
+        x = activations(rows, cols, dtype, 10 + k)
+        want, scales = ref.checkpoint(to64(x), fmt)
+        for view in (x.cuda(), strided(x.cuda(), cols + 3)):
+            c = nsm.checkpoint_pack(view, format=fmt)
+            assert c.shape == (rows, cols) and c.format == fmt
+            np.testing.assert_array_equal(c.scales.cpu().numpy(), scales)
+            assert not c.codes[:, cols:].any()
+            np.testing.assert_array_equal(to64(nsm.checkpoint_unpack(c, dtype=torch.float32)), want)
+            np.testing.assert_array_equal(to64(nsm.checkpoint_unpack(c)), want)          # exact in bf16 too
+            half = torch.from_numpy(want).clamp(-65504, 65504).to(torch.float16)
+            np.testing.assert_array_equal(to64(nsm.checkpoint_unpack(c, dtype=torch.float16)), half.double().numpy())
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_pack_edges_of_the_range(nsm, fmt):
+    big = 3.4028234663852886e38
+    x = torch.zeros(12, 64)
+    x[1] = 2.0 ** -140                                  # below the smallest scale's codes
+    x[2] = -2.0 ** -112
+    x[3, 5] = big
+    x[4, 40] = -big / 2
+    x[5, 3], x[6, 63], x[7, 0] = math.inf, math.nan, -math.inf
+    x[8] = torch.linspace(-500, 500, 64)
+    x[9, 0], x[9, 1:32] = ref.LARGEST[fmt], torch.arange(31) / 2.0       # half steps of the whole-number grid
+    x[10, 32:] = torch.tensor([1.0, 1.0625, 1.1875, 448.0] * 8)         # half steps of the e4m3 grid
+    x[11] = 65504.0
+    want, scales = ref.checkpoint(to64(x), fmt)
+    c = nsm.checkpoint_pack(x.cuda(), format=fmt)
+    np.testing.assert_array_equal(c.scales.cpu().numpy(), scales)
+    np.testing.assert_array_equal(to64(nsm.checkpoint_unpack(c, dtype=torch.float32)), want)
+    assert np.isnan(want[5, :32]).all() and np.isfinite(want[5, 32:]).all()
+    got = to64(nsm.checkpoint_unpack(c, dtype=torch.float16))
+    assert np.nanmax(np.abs(got)) == 65504.0 and np.isnan(got[6, 32:]).all()
+
+
+def test_every_byte_decodes(nsm):
+    """All 256 codes under all 256 exponent bytes."""
+    codes = torch.arange(256, dtype=torch.uint8).repeat(256, 1)
+    scales = torch.arange(256, dtype=torch.uint8)[:, None].repeat(1, 8)
+    for fmt in ("e4m3", "int8"):
+        want = torch.from_numpy(ref.values(codes.numpy(), scales.numpy(), 256, fmt)).float().double().numpy()
+        got = to64(nsm.checkpoint_unpack(nsm.Checkpoint(codes.cuda(), scales.cuda(), 256, fmt), dtype=torch.float32))
+        keep = (np.abs(want) >= 2.0 ** -126) | (want == 0) | np.isnan(want)      # subnormal fp32 may be flushed
+        assert np.array_equal(np.isnan(got), np.isnan(want))
+        ok = keep & ~np.isnan(want)
+        np.testing.assert_array_equal(got[ok], want[ok])
+
+
+def test_pack_writes_only_its_bytes(nsm):
+    codes = torch.full((6, 64), 77, dtype=torch.uint8, device="cuda")
+    scales = torch.full((6, 5), 77, dtype=torch.uint8, device="cuda")
+    out = nsm.Checkpoint(codes[1:5, :48], scales[1:5, :2], 34, "int8")
+    nsm.checkpoint_pack(activations(4, 34, "bf16", 1).cuda(), out=out)
+    c, s = codes.cpu(), scales.cpu()
+    assert (c[0] == 77).all() and (c[5] == 77).all() and (c[1:5, 48:] == 77).all() and not c[1:5, 34:48].any()
+    assert (s[0] == 77).all() and (s[5] == 77).all() and (s[1:5, 2:] == 77).all()
+    wide = torch.full((4, 40), 5.0, device="cuda")
+    nsm.checkpoint_unpack(out, out=wide[:, 1:35])
+    assert (wide[:, 0] == 5).all() and (wide[:, 35:] == 5).all()
+
+
+def test_checkpoint_beyond_32_bit_offsets(nsm):
+    """Codes of 2.3e9 bytes: the last rows read and write where they belong."""
+    rows, cols = 1150003, 2000
+    x = torch.empty(rows, cols, dtype=torch.float16, device="cuda").fill_(0.25)
+    tail = activations(70, cols, "f16", 3).cuda()
+    x[-70:] = tail
+    c, small = nsm.checkpoint_pack(x), nsm.checkpoint_pack(tail)
+    assert torch.equal(c.codes[-70:], small.codes) and torch.equal(c.scales[-70:], small.scales)
+    assert torch.equal(c.codes[:3], nsm.checkpoint_pack(x[:3]).codes)
+    nsm.checkpoint_unpack(c, out=x)
+    assert torch.equal(x[-70:], nsm.checkpoint_unpack(small, dtype=torch.float16))
+    rows_of = torch.arange(rows - 70, rows, dtype=torch.int32, device="cuda")
+    dy = activations(70, 40, "bf16", 4).cuda()
+    assert torch.equal(nsm.checkpoint_wgrad(dy, c, rows=rows_of), nsm.checkpoint_wgrad(dy, small))
+
+
+def swiglu_slack(g, factor):
+    """fp32 arithmetic: under 16 roundings, and the exponential's argument
+    carries its own (|g| steps)."""
+    return factor * 16 * (1 + np.abs(g)) * U32
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 33), (5, 768), (67, 517)])
+def test_swiglu_forward_and_backward(nsm, rows, cols, dtype, fmt):
+    both = (3 * torch.randn(rows, 2 * cols, generator=torch.Generator().manual_seed(rows))).to(DT[dtype])
+    both[0, 0] = -30.0
+    gate, up = both.cuda()[:, :cols], both.cuda()[:, cols:]          # halves of one projection
+    h, cg, cu = nsm.checkpoint_swiglu(gate, up, format=fmt)
+    g, u = to64(gate), to64(up)
+    want = ref.swiglu(g, u)
+    near(h, want, half_step(want, dtype) + swiglu_slack(g, np.abs(want)), "h")
+    for saved, x in ((cg, g), (cu, u)):
+        np.testing.assert_array_equal(to64(nsm.checkpoint_unpack(saved, dtype=torch.float32)), ref.checkpoint(x, fmt)[0])
+    d = activations(rows, cols, dtype, 5)
+    gq, uq = ref.checkpoint(g, fmt)[0], ref.checkpoint(u, fmt)[0]
+    want_g, want_u, want_h = ref.swiglu_backward(to64(d), gq, uq)
+    grad = torch.full((rows, 2 * cols + 1), 7.0, dtype=DT[dtype], device="cuda")
+    gg, gu, again = nsm.checkpoint_swiglu_backward(d.cuda(), cg, cu, grad_gate=grad[:, :cols], grad_up=grad[:, cols:-1])
+    s = ref.sigmoid(gq)
+    near(gg, want_g, half_step(want_g, dtype) + swiglu_slack(gq, np.abs(to64(d) * uq * s) * (1 + np.abs(gq))), "grad_gate")
+    near(gu, want_u, half_step(want_u, dtype) + swiglu_slack(gq, np.abs(want_u)), "grad_up")
+    near(again, want_h, half_step(want_h, dtype) + swiglu_slack(gq, np.abs(want_h)), "h again")
+    assert (grad[:, -1] == 7).all()
+    two = nsm.checkpoint_swiglu_backward(d.cuda(), cg, cu, recompute=False)
+    assert two[2] is None and torch.equal(two[0], gg) and torch.equal(two[1], gu)
+
+
+def test_swiglu_extreme_gates(nsm):
+    gate = torch.tensor([[-200.0, -88.0, 0.0, 88.0, 200.0, 1e30, -1e30, 0.5]]).cuda()
+    up = torch.ones_like(gate)
+    h, cg, cu = nsm.checkpoint_swiglu(gate, up)
+    g = to64(gate)
+    want = ref.swiglu(g, np.ones_like(g))
+    near(h, want, half_step(want, "f32") + swiglu_slack(np.clip(g, -100, 100), np.abs(want)) + 1e-36, "h")
+    bad = gate.clone()
+    bad[0, 2] = math.nan
+    h, cg, cu = nsm.checkpoint_swiglu(bad, up)
+    assert torch.isnan(h[0, 2]) and torch.isfinite(h[0, :2]).all()
+    gg, gu, again = nsm.checkpoint_swiglu_backward(up, cg, cu)
+    assert torch.isnan(gg).all() and torch.isnan(gu).all()           # the whole block is marked
+
+
+# ---------------------------------------------------------------- weight gradients
+
+def wgrad_tolerance(dy, x, out_dtype, want, **lists):
+    """Sums of n products in fp32, whatever their order: n roundings of at most
+    the sum of magnitudes each (one more for joining parts)."""
+    size = ref.wgrad(np.abs(dy), np.abs(x), **lists)
+    return half_step(want, out_dtype) + (dy.shape[0] + 4) * U32 * size
+
+
+def operand(ckpt64, dtype):
+    """The 16-bit operand that a checkpoint's values become."""
+    if dtype == "bf16":
+        return ckpt64
+    return torch.from_numpy(ckpt64).clamp(-65504, 65504).to(torch.float16).double().numpy()
+
+
+@pytest.mark.parametrize("tokens,outs,cols", [(1, 1, 1), (3, 5, 7), (31, 130, 33), (33, 64, 128), (65, 257, 129), (97, 128, 300),
+                                              (300, 260, 514), (1000, 40, 64), (2048, 192, 192), (5003, 72, 48)])
+@pytest.mark.parametrize("dtype,fmt,out_dtype,transposed", [("bf16", "e4m3", "f32", False), ("bf16", "int8", "bf16", True),
+                                                            ("f16", "e4m3", "f16", True), ("f16", "int8", "f32", False),
+                                                            ("bf16", "e4m3", "f32", True), ("f16", "int8", "bf16", False)])
+def test_wgrad(nsm, tokens, outs, cols, dtype, fmt, out_dtype, transposed):
+    x, dy = activations(tokens, cols, dtype, 7), (0.1 * activations(tokens, outs, dtype, 8).float()).to(DT[dtype])
+    c = nsm.checkpoint_pack(x.cuda(), format=fmt)
+    xq = operand(ref.checkpoint(to64(x), fmt)[0], dtype)
+    want = to64(dy).T @ xq
+    want = want.T if transposed else want
+    size = np.abs(to64(dy)).T @ np.abs(xq)
+    tol = half_step(want, out_dtype) + (tokens + 4) * U32 * (size.T if transposed else size)
+    got = nsm.checkpoint_wgrad(dy.cuda(), c, out_dtype=DT[out_dtype], transposed=transposed)
+    assert got.dtype == DT[out_dtype]
+    near(got, want, tol, "dW")
+    again = nsm.checkpoint_wgrad(strided(dy.cuda(), outs + 1), c, out_dtype=DT[out_dtype], transposed=transposed)
+    assert torch.equal(again, got)                                   # strides change nothing, and runs are bitwise equal
+    base = activations(*got.shape, out_dtype, 9).cuda()
+    total = to64(base) + want
+    acc = nsm.checkpoint_wgrad(dy.cuda(), c, out=base, transposed=transposed, accumulate=True)
+    assert acc is base
+    near(base, total, tol + half_step(total, out_dtype) + U32 * np.abs(total), "dW added")
+
+
+@pytest.mark.parametrize("dtype,transposed", [("bf16", False), ("f16", True)])
+@pytest.mark.parametrize("outs,cols", [(33, 65), (192, 256), (257, 40)])
+def test_wgrad_of_experts(nsm, outs, cols, dtype, transposed):
+    """Ragged experts, some without slots, gathered rows with repeats and rows
+    left out, and slots past the last offset that are never read."""
+    tokens, sizes = 150, [0, 1, 70, 0, 31, 32, 33, 0]
+    slots = sum(sizes) + 9
+    gen = torch.Generator().manual_seed(11)
+    x, dy = activations(tokens, cols, dtype, 12), (0.1 * activations(slots, outs, dtype, 13).float()).to(DT[dtype])
+    rows = torch.randint(0, tokens, (slots,), generator=gen, dtype=torch.int32)
+    rows[5], rows[6], rows[40], rows[41] = -1, tokens, rows[39], 2 ** 31 - 1
+    dy[5] = math.inf                                                 # belongs to a slot that is left out
+    dy[sum(sizes):] = math.nan
+    offsets = torch.tensor([0] + list(np.cumsum(sizes)), dtype=torch.int32)
+    c = nsm.checkpoint_pack(x.cuda())
+    xq = operand(ref.checkpoint(to64(x), "e4m3")[0], dtype)
+    clean = to64(dy)
+    clean[5] = 0.0
+    clean[sum(sizes):] = 0.0
+    lists = dict(offsets=offsets.numpy(), rows=rows.numpy(), transposed=transposed)
+    want = ref.wgrad(clean, xq, **lists)
+    tol = wgrad_tolerance(clean, xq, "f32", want, **lists)
+    got = nsm.checkpoint_wgrad(dy.cuda(), c, offsets=offsets.cuda(), rows=rows.cuda(), transposed=transposed)
+    near(got, want, tol, "dW of experts")
+    assert not got[0].any() and not got[7].any()
+    kept = torch.full_like(got, 3.0)
+    nsm.checkpoint_wgrad(dy.cuda(), c, out=kept, offsets=offsets.cuda(), rows=rows.cuda(), transposed=transposed, accumulate=True)
+    assert (kept[0] == 3).all() and (kept[3] == 3).all()
+
+
+def test_wgrad_offsets_out_of_range_are_clamped(nsm):
+    x, dy = activations(40, 32, "bf16", 1), activations(40, 32, "bf16", 2)
+    c = nsm.checkpoint_pack(x.cuda())
+    offsets = torch.tensor([-5, 10, 4, 90, 2 ** 31 - 1], dtype=torch.int32)
+    got = nsm.checkpoint_wgrad(dy.cuda(), c, offsets=offsets.cuda())
+    xq = ref.checkpoint(to64(x), "e4m3")[0]
+    want = ref.wgrad(to64(dy), xq, offsets=offsets.numpy())
+    near(got, want, wgrad_tolerance(to64(dy), xq, "f32", want, offsets=offsets.numpy()), "dW")
+
+
+def test_wgrad_without_tokens_and_marked_blocks(nsm):
+    c = nsm.checkpoint_pack(torch.empty(0, 40, device="cuda"))
+    out = torch.full((24, 40), 2.0, device="cuda")
+    dy = torch.empty(0, 24, dtype=torch.bfloat16, device="cuda")
+    nsm.checkpoint_wgrad(dy, c, out=out, accumulate=True)
+    assert (out == 2).all()
+    assert not nsm.checkpoint_wgrad(dy, c, out=out).any()
+    x = torch.ones(9, 70, device="cuda")
+    x[4, 33] = math.inf
+    got = nsm.checkpoint_wgrad(torch.ones(9, 5, dtype=torch.bfloat16, device="cuda"), nsm.checkpoint_pack(x))
+    assert torch.isnan(got[:, 32:64]).all() and (got[:, :32] == 9).all() and (got[:, 64:] == 9).all()
+
+
+def test_wgrad_rows_far_apart(nsm):
+    """grad_y rows 2^25 elements apart: 80 rows pass 2^31 elements."""
+    ld, tokens, outs, cols = 1 << 25, 80, 24, 64
+    wide = torch.empty(tokens * ld, dtype=torch.bfloat16, device="cuda")
+    dy = wide.as_strided((tokens, outs), (ld, 1))
+    small = activations(tokens, outs, "bf16", 3).cuda()
+    dy.copy_(small)
+    c = nsm.checkpoint_pack(activations(tokens, cols, "bf16", 4).cuda())
+    assert torch.equal(nsm.checkpoint_wgrad(dy, c), nsm.checkpoint_wgrad(small, c))
+
+
+# ---------------------------------------------------------------- routing
+
+ROUTES = [
+    dict(tokens=1, experts=1, top_k=1),
+    dict(tokens=5, experts=64, top_k=6, dtype="bf16"),
+    dict(tokens=63, experts=7, top_k=7, score="sigmoid", renormalize=False),
+    dict(tokens=65, experts=65, top_k=3, bias=True, dtype="f16", mask=True),
+    dict(tokens=200, experts=256, top_k=8, score="sigmoid", bias=True, groups=8, top_groups=4, scale=2.5, mask=True),
+    dict(tokens=130, experts=96, top_k=4, groups=6, top_groups=2, group_top=1, dtype="bf16"),
+    dict(tokens=70, experts=60, top_k=5, bias=True, groups=60, top_groups=20, dtype="bf16"),
+    dict(tokens=31, experts=500, top_k=20, bias=True, score="sigmoid"),
+    dict(tokens=9, experts=1024, top_k=64, renormalize=False, groups=64, top_groups=5, bias=True),
+    dict(tokens=1500, experts=64, top_k=6, bias=True, dtype="bf16", mask=True),
+]
+
+
+def route_inputs(case, seed=21):
+    gen = torch.Generator().manual_seed(seed)
+    dtype = DT[case.get("dtype", "f32")]
+    logits = (1.5 * torch.randn(case["tokens"], case["experts"], generator=gen)).to(dtype)
+    bias = 0.1 * torch.randn(case["experts"], generator=gen) if case.get("bias") else None
+    mask = torch.rand(case["tokens"], generator=gen) < 0.8 if case.get("mask") else None
+    kw = {k: case[k] for k in ("score", "groups", "top_groups", "group_top", "renormalize", "scale") if k in case}
+    return logits, bias, mask, kw
+
+
+def check_route(nsm, logits, top_k, bias, mask, kw):
+    want = ref.route(to64(logits), top_k, bias=None if bias is None else to64(bias), token_mask=None if mask is None else mask.numpy(), **kw)
+    gpu = dict(bias=None if bias is None else bias.cuda(), token_mask=None if mask is None else mask.cuda(), **kw)
+    got = nsm.route(logits.cuda(), top_k, **gpu)
+    for key in ("experts", "counts", "offsets", "order", "rows"):
+        np.testing.assert_array_equal(getattr(got, key).cpu().numpy(), want[key], err_msg=key)
+    # a weight is a quotient of sums of exponentials: under 32 fp32 roundings
+    near(got.weights, want["weights"], np.abs(want["weights"]) * 32 * U32 + 1e-37, "weights")
+    bare = nsm.route(logits.cuda(), top_k, dispatch=False, **gpu)
+    assert torch.equal(bare.experts, got.experts) and torch.equal(bare.weights.view(torch.int32), got.weights.view(torch.int32))
+    assert bare.order is None
+    return got, want
+
+
+@pytest.mark.parametrize("case", ROUTES, ids=lambda c: "%dx%d" % (c["tokens"], c["experts"]))
+def test_route(nsm, case):
+    logits, bias, mask, kw = route_inputs(case)
+    check_route(nsm, logits, case["top_k"], bias, mask, kw)
+    wide = strided(logits.cuda(), case["experts"] + 5)
+    a = nsm.route(wide, case["top_k"], bias=None if bias is None else bias.cuda(), token_mask=None if mask is None else mask.cuda(), **kw)
+    b = nsm.route(logits.cuda(), case["top_k"], bias=None if bias is None else bias.cuda(), token_mask=None if mask is None else mask.cuda(), **kw)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_ties_and_masked_experts(nsm, score, biased):
+    """Equal logits, experts masked by -inf (all, all but one, some), the
+    type's lowest value, NaN and +inf; bias makes near-equal choices."""
+    low = torch.finfo(torch.float32).min
+    logits = torch.zeros(20, 40)
+    logits[1] = -math.inf
+    logits[2, :39] = -math.inf
+    logits[3, ::2] = -math.inf
+    logits[4] = low
+    logits[5, 1:] = low
+    logits[6, 7] = math.nan
+    logits[7, 9] = math.inf
+    logits[8] = torch.arange(40) // 4
+    logits[9] = 60.0 + torch.arange(40)                 # sigmoids that all round to 1
+    logits[10] = -torch.arange(40) * 30.0
+    logits[11, 3], logits[11, 30] = 1.0, 1.0 + 2.0 ** -23
+    logits[12, 30], logits[12, 3] = 1.0, 1.0 + 2.0 ** -23
+    logits[13:] = torch.randn(7, 40, generator=torch.Generator().manual_seed(2)).round()
+    bias = None
+    if biased:
+        bias = torch.zeros(40)
+        bias[5], bias[6], bias[7], bias[8] = 2.0 ** -26, math.nan, -math.inf, -2.0 ** -30
+    mask = torch.ones(20, dtype=torch.bool)
+    mask[19] = False
+    for kw in (dict(), dict(groups=8, top_groups=3), dict(groups=10, top_groups=2, group_top=1, renormalize=False)):
+        check_route(nsm, logits, 8, bias, mask, dict(score=score, **kw))
+
+
+def test_route_choices_closer_than_fp32(nsm):
+    """Choices that differ by less than fp32 shows: score + bias pairs whose
+    order is decided by their 64-bit values."""
+    gen = torch.Generator().manual_seed(5)
+    logits = torch.randn(400, 64, generator=gen)
+    logits[:, 1:] = logits[:, :1]
+    logits += torch.randint(-3, 4, (400, 64), generator=gen) * 2.0 ** -22
+    bias = torch.randint(-3, 4, (64,), generator=gen).float() * 2.0 ** -25
+    for score in ("sigmoid", "softmax"):
+        check_route(nsm, logits, 6, bias, None, dict(score=score))
+        check_route(nsm, logits, 6, bias, None, dict(score=score, groups=8, top_groups=3))
+
+
+def test_route_load_and_empty_batch(nsm):
+    load = torch.full((64,), 5, dtype=torch.int64, device="cuda")
+    total = load.clone()
+    for tokens in (40, 700, 0):
+        logits = torch.randn(tokens, 64, generator=torch.Generator().manual_seed(tokens)).cuda()
+        r = nsm.route(logits, 4, load=load)
+        total += r.counts
+        assert torch.equal(load, total) and int(r.offsets[-1]) == tokens * 4
+    assert r.order.numel() == 0 and not r.counts.any()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("tokens,experts,top_k,dtype", [(1, 1, 1, "f32"), (5, 64, 6, "bf16"), (67, 100, 3, "f32"), (130, 256, 8, "f16"),
+                                                        (9, 1000, 64, "f32"), (64, 8, 8, "bf16")])
+def test_route_backward(nsm, tokens, experts, top_k, dtype, score, renormalize):
+    gen = torch.Generator().manual_seed(31)
+    logits = (1.5 * torch.randn(tokens, experts, generator=gen)).to(DT[dtype])
+    ids = torch.stack([torch.randperm(experts, generator=gen)[:top_k] for _ in range(tokens)]).to(torch.int32)
+    dw = torch.randn(tokens, top_k, generator=gen)
+    if tokens > 4:
+        ids[0], ids[1, 0], dw[0, 0] = -1, -1, math.nan      # a token without experts: its incoming gradient is not read
+        ids[2, 1] = ids[2, 0]                               # the same expert twice
+        ids[3, 0] = experts + 3
+        logits[4, (int(ids[4, 0]) + 1) % experts] = -math.inf
+    got = nsm.route_backward(dw.cuda(), strided(logits.cuda(), experts + 2), ids.cuda(), score=score, renormalize=renormalize, scale=1.5)
+    want = ref.route_backward(to64(dw), to64(logits), ids.numpy(), score, renormalize, 1.5)
+    # scores carry under 32 roundings, and the gradient of a weight at most
+    # twice the largest incoming one over the scores' sum; 64 in all
+    s = np.stack([ref._scores(r, score) for r in to64(logits)])
+    z = np.ones((tokens, 1))
+    if renormalize:
+        z = np.array([max(sum(s[t, i] for i in ids[t].tolist() if 0 <= i < experts), 1e-30) for t in range(tokens)])[:, None]
+    top = np.nan_to_num(np.abs(to64(dw))).max(axis=1, keepdims=True)
+    near(got, want, half_step(want, dtype) + 64 * U32 * s * 2 * 1.5 * top / z * top_k, "grad_logits")
+
+
+def test_route_then_backward_of_poisoned_tokens(nsm):
+    logits = torch.zeros(3, 8)
+    logits[1, 2] = math.nan
+    r = nsm.route(logits.cuda(), 2)
+    g = nsm.route_backward(torch.ones(3, 2, device="cuda"), logits.cuda(), r.experts, renormalize=False)
+    assert torch.isnan(r.weights[1]).all() and not g[1].any() and torch.isfinite(g).all()
+
+
+@pytest.mark.parametrize("layers,experts", [(1, 1), (1, 64), (24, 64), (3, 257), (2, 1000)])
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_balance_step(nsm, layers, experts, dtype):
+    gen = torch.Generator().manual_seed(layers)
+    bias = torch.randn(layers, experts, generator=gen)
+    counts = torch.randint(0, 5, (layers, experts), generator=gen).to(dtype)
+    if dtype == torch.int64:
+        counts += 3 << 32
+    else:
+        counts[0] = 2 ** 31 - 1 if layers > 1 else counts[0]
+    got = bias.cuda()
+    nsm.balance_step(got, counts.cuda(), rate=0.001)
+    sign = np.sign(ref.balance(np.zeros((layers, experts)), counts.numpy(), 1.0))
+    want = bias + torch.from_numpy(sign).float() * torch.tensor(0.001)
+    assert torch.equal(got.cpu(), want)
+    row = bias[0].cuda()
+    nsm.balance_step(row, counts[0].cuda(), rate=0.001)
+    assert torch.equal(row.cpu(), want[0])
+
+
+# ---------------------------------------------------------------- together
+
+def layer_step(nsm, state):
+    """One expert layer's part of a training step: route, keep the input in 8
+    bits, SwiGLU's backward, the experts' weight gradients, and the updates."""
+    r = nsm.route(state["logits"], 2, bias=state["bias"], score="sigmoid", token_mask=state["mask"])
+    saved = nsm.checkpoint_pack(state["x"])
+    h, cg, cu = nsm.checkpoint_swiglu(state["gate"], state["up"])
+    gg, gu, again = nsm.checkpoint_swiglu_backward(state["grad_h"], cg, cu)
+    dw_up = nsm.checkpoint_wgrad(gu, saved, out_dtype=torch.bfloat16, transposed=True, offsets=r.offsets, rows=r.rows)
+    dw_down = nsm.checkpoint_wgrad(state["grad_y"], nsm.checkpoint_pack(again), out_dtype=torch.bfloat16, transposed=True, offsets=r.offsets)
+    grad_logits = nsm.route_backward(state["grad_weights"], state["logits"], r.experts, score="sigmoid")
+    dw_router = nsm.checkpoint_wgrad(grad_logits, saved, out_dtype=torch.bfloat16)
+    nsm.balance_step(state["bias"], r.counts, rate=0.001)
+    params = [dict(p, grad=g) for p, g in zip(state["params"], list(dw_up) + list(dw_down) + [dw_router])]
+    nsm.muon_step(params, lr=0.02, mu=0.95, ns_dtype="bf16", workspace=state["workspace"])
+    return [h, gg, gu, again, dw_up, dw_down, grad_logits, *r]
+
+
+def layer_state(nsm, seed):
+    gen = torch.Generator().manual_seed(seed)
+    tokens, d, f, experts = 257, 96, 160, 4
+
+    def bf(*shape, scale=1.0):
+        return (scale * torch.randn(*shape, generator=gen)).to(torch.bfloat16).cuda()
+
+    shapes = [(d, f)] * experts + [(f, d)] * experts + [(experts, d)]
+    params = [{"weight": torch.randn(*s, generator=gen).cuda(), "momentum": torch.zeros(*s, device="cuda")} for s in shapes]
+    dummy = [dict(p, grad=torch.empty(*s, dtype=torch.bfloat16, device="cuda")) for p, s in zip(params, shapes)]
+    need = nsm.muon_workspace_size(dummy, ns_dtype="bf16")
+    return {"logits": bf(tokens, experts), "bias": (0.05 * torch.randn(experts, generator=gen)).cuda(),
+            "mask": (torch.rand(tokens, generator=gen) < 0.9).cuda(), "x": bf(tokens, d), "gate": bf(tokens * 2, f), "up": bf(tokens * 2, f),
+            "grad_h": bf(tokens * 2, f, scale=0.1), "grad_y": bf(tokens * 2, d, scale=0.1),
+            "grad_weights": torch.randn(tokens, 2, generator=gen).cuda(), "params": params,
+            "workspace": torch.empty(need, dtype=torch.uint8, device="cuda")}
+
+
+def copy_state(state):
+    out = {k: (v.clone() if isinstance(v, torch.Tensor) else v) for k, v in state.items()}
+    out["params"] = [{k: v.clone() for k, v in p.items()} for p in state["params"]]
+    return out
+
+
+def same_bits(a, b):
+    return a.dtype == b.dtype and torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_a_layer_step_against_its_definition(nsm):
+    state = layer_state(nsm, 41)
+    before = copy_state(state)
+    out = layer_step(nsm, state)
+    want = ref.route(to64(before["logits"]), 2, bias=to64(before["bias"]), score="sigmoid", token_mask=before["mask"].cpu().numpy())
+    np.testing.assert_array_equal(out[7].cpu().numpy(), want["experts"])
+    np.testing.assert_array_equal(out[10].cpu().numpy(), want["offsets"])
+    gq, uq = (ref.checkpoint(to64(before[k]), "e4m3")[0] for k in ("gate", "up"))
+    _, _, again = ref.swiglu_backward(to64(before["grad_h"]), gq, uq)
+    xq, hq = ref.checkpoint(to64(before["x"]), "e4m3")[0], ref.checkpoint(to64(out[3]), "e4m3")[0]
+    near(out[3], again, half_step(again, "bf16") + swiglu_slack(gq, np.abs(again)), "h")
+    lists = dict(offsets=want["offsets"], rows=want["rows"], transposed=True)
+    dw = ref.wgrad(to64(out[2]), xq, **lists)
+    near(out[4], dw, wgrad_tolerance(to64(out[2]), xq, "bf16", dw, **lists), "dW up")
+    lists.pop("rows")
+    dw = ref.wgrad(to64(before["grad_y"]), hq, **lists)
+    near(out[5], dw, wgrad_tolerance(to64(before["grad_y"]), hq, "bf16", dw, **lists), "dW down")
+    np.testing.assert_allclose(to64(state["bias"]), ref.balance(to64(before["bias"]), want["counts"], 0.001), rtol=0, atol=2.0 ** -24)
+    for p, q in zip(state["params"], before["params"]):
+        assert torch.isfinite(p["weight"]).all() and not torch.equal(p["weight"], q["weight"])
+
+
+def test_layer_steps_captured_and_replayed(nsm):
+    """The whole step in a HIP graph, replayed with eager work between, against
+    eager steps from the same state."""
+    state = layer_state(nsm, 42)
+    eager = copy_state(state)
+    layer_step(nsm, copy_state(state))                 # warm-up on scratch state
+    torch.cuda.synchronize()
+    start = copy_state(state)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer_step(nsm, state)
+    for k, v in start.items():
+        if isinstance(v, torch.Tensor) and k != "workspace":
+            state[k].copy_(v)
+    for p, q in zip(state["params"], start["params"]):
+        for key in p:
+            p[key].copy_(q[key])
+    for i in range(4):
+        want = layer_step(nsm, eager)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert same_bits(a, b), "replay %d" % i
+        for p, q in zip(state["params"], eager["params"]):
+            assert same_bits(p["weight"], q["weight"]) and same_bits(p["momentum"], q["momentum"])
+        assert same_bits(state["bias"], eager["bias"])
+        nsm.checkpoint_wgrad(eager["grad_y"], nsm.checkpoint_pack(eager["gate"]))
+
+
+def test_calls_on_two_streams_do_not_mix(nsm):
+    states = [layer_state(nsm, 50 + i) for i in range(2)]
+    want = [layer_step(nsm, copy_state(s)) for s in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    got = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(states):
+            with torch.cuda.stream(streams[i]):
+                got[i] = layer_step(nsm, copy_state(s))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(same_bits(x, y) for x, y in zip(a, b))
+
+
+def test_refusals_enqueue_nothing(nsm):
+    x = torch.ones(4, 64, device="cuda")
+    with pytest.raises(ValueError, match="unit column stride"):
+        nsm.checkpoint_pack(x.t())
+    with pytest.raises(ValueError, match="shape"):
+        nsm.checkpoint_swiglu(x, x[:, :32])
+    with pytest.raises(ValueError, match="format"):
+        nsm.checkpoint_pack(x, format="int4")
+    c = nsm.checkpoint_pack(x)
+    with pytest.raises(nsm.MuonError, match="F16 or BF16"):
+        nsm.checkpoint_wgrad(x, c)
+    dy = x.bfloat16()
+    with pytest.raises(nsm.MuonError, match="need rows_of"):
+        nsm.checkpoint_wgrad(dy[:3], c)
+    with pytest.raises(ValueError, match="accumulate"):
+        nsm.checkpoint_wgrad(dy, c, accumulate=True)
+    with pytest.raises(nsm.MuonError, match="overlap"):
+        nsm.checkpoint_swiglu(x, x * 2, out=x)
+    with pytest.raises(nsm.MuonError, match="groups"):
+        nsm.route(x, 2, groups=3, top_groups=1)
+    with pytest.raises(nsm.MuonError, match="top_k"):
+        nsm.route(x, 65)
+    with pytest.raises(ValueError, match="int32"):
+        nsm.route_backward(torch.ones(4, 2, device="cuda"), x, torch.zeros(4, 2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError, match="int32 or int64"):
+        nsm.balance_step(x[0], x[0], rate=0.1)
+    torch.cuda.synchronize()
+    assert (x == 1).all()

@@ -1,0 +1,311 @@
+"""The training operators' C entry points without a GPU: struct layouts, every
+refusal (reported before anything would be enqueued), workspace sizes, and the
+host code under AddressSanitizer and UndefinedBehaviorSanitizer."""
+import ctypes
+import math
+import os
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+from conftest import ROOT
+import newton_schulz_matrix_momentum_amd as nsm
+from newton_schulz_matrix_momentum_amd import _lib
+
+INCLUDE = os.path.join(ROOT, "include")
+CSRC = os.path.join(ROOT, "newton_schulz_matrix_momentum_amd", "csrc")
+E, U, SMALL, OK = _lib.MUON_ERR_INVALID_ARG, _lib.MUON_ERR_UNSUPPORTED, _lib.MUON_ERR_WORKSPACE_TOO_SMALL, _lib.MUON_OK
+F32, F16, BF16 = _lib.MUON_F32, _lib.MUON_F16, _lib.MUON_BF16
+BASE = 1 << 40       # fake device addresses: refusals come before any pointer is touched
+STEP = 1 << 36
+
+
+def at(i):
+    return BASE + i * STEP
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _lib.load()
+
+
+def test_struct_layouts_match_the_header(tmp_path):
+    structs = {"muon_ckpt": _lib.MuonCkpt, "muon_wgrad": _lib.MuonWgrad, "muon_routing": _lib.MuonRouting}
+    lines = []
+    for name, cls in structs.items():
+        lines.append('printf("%%zu\\n", sizeof(%s));' % name)
+        lines += ['printf("%%zu\\n", offsetof(%s, %s));' % (name, f[0]) for f in cls._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "muon.h"\nint main(void) {\n%s\n'
+                   'printf("%%d\\n", MUON_CKPT_BLOCK); return 0; }\n' % "\n".join(lines))
+    exe = tmp_path / "layout"
+    subprocess.check_call(["gcc", "-std=c99", "-Wall", "-I", INCLUDE, str(src), "-o", str(exe)])
+    got = [int(v) for v in subprocess.check_output([str(exe)]).split()]
+    want = []
+    for cls in structs.values():
+        want.append(ctypes.sizeof(cls))
+        want += [getattr(cls, f[0]).offset for f in cls._fields_]
+    assert got == want + [_lib.CKPT_BLOCK]
+
+
+def ckpt(i=0, rows=8, cols=40, codes_ld=48, scales_ld=2, fmt=0):
+    return _lib.MuonCkpt(at(i), at(i + 1), rows, cols, codes_ld, scales_ld, fmt)
+
+
+def pack(lib, c, x=at(10), ld=40, dtype=BF16):
+    return lib.muon_ckpt_pack(x, ld, dtype, c, None)
+
+
+def test_checkpoint_refusals(lib):
+    bad = [
+        (dict(c=ckpt(cols=0)), E), (dict(c=ckpt(rows=-1)), E), (dict(c=ckpt(fmt=2)), U), (dict(c=ckpt(codes_ld=47)), E),
+        (dict(c=ckpt(codes_ld=32)), E), (dict(c=ckpt(scales_ld=1)), E), (dict(c=ckpt(cols=(1 << 20) + 1, codes_ld=1 << 21, scales_ld=1 << 20), ld=1 << 21), U),
+        (dict(c=ckpt(rows=1 << 30)), U), (dict(c=ckpt(), dtype=7), U), (dict(c=ckpt(), ld=39), E), (dict(c=ckpt(), x=at(10) + 1), E),
+        (dict(c=ckpt(), x=None), E), (dict(c=ckpt(), x=at(0) + 16), E),
+    ]
+    for kw, status in bad:
+        assert pack(lib, **kw) == status, (kw, _lib.last_error())
+    c = ckpt()
+    c.codes += 8
+    assert pack(lib, c) == E and "aligned" in _lib.last_error()
+    c = ckpt()
+    c.scales = c.codes + 7 * 48 + 47
+    assert pack(lib, c) == E and "overlap" in _lib.last_error()
+    assert lib.muon_ckpt_pack(at(10), 40, BF16, None, None) == E
+    assert pack(lib, ckpt(rows=0)) == OK
+    assert lib.muon_ckpt_pack(None, 40, BF16, _lib.MuonCkpt(None, None, 0, 40, 48, 2, 0), None) == OK
+    assert lib.muon_ckpt_unpack(ckpt(), None, 40, BF16, None) == E
+    assert lib.muon_ckpt_unpack(ckpt(), at(1) - 2, 40, BF16, None) == E
+    assert lib.muon_ckpt_unpack(ckpt(rows=0), None, 40, BF16, None) == OK
+    assert lib.muon_last_error() == b""
+
+
+def test_swiglu_refusals(lib):
+    def fwd(g=at(10), u=at(11), h=at(12), cg=None, cu=None, lds=(40, 40, 40), dtype=BF16):
+        return lib.muon_ckpt_swiglu(g, lds[0], u, lds[1], dtype, h, lds[2], cg or ckpt(0), cu or ckpt(2), None)
+
+    assert fwd(cu=ckpt(2, rows=7)) == E and fwd(cu=ckpt(2, fmt=1)) == E and fwd(cu=ckpt(2, cols=39)) == E
+    assert fwd(dtype=5) == U and fwd(h=None) == E and fwd(lds=(40, 39, 40)) == E and fwd(u=None) == E
+    assert fwd(h=at(10) + 2) == E and "overlap" in _lib.last_error()
+    assert fwd(cu=ckpt(0)) == E
+    # an output in the other columns of a wider matrix does not overlap, one column further it does
+    rows = dict(cg=ckpt(0, rows=0), cu=ckpt(2, rows=0))
+    assert fwd(g=at(10), u=at(10) + 80, h=at(12), lds=(80, 80, 40), **rows) == OK
+
+    def back(d=at(10), gg=at(11), gu=at(12), h=at(13), lds=(40, 40, 40, 40)):
+        return lib.muon_ckpt_swiglu_backward(d, lds[0], BF16, ckpt(0), ckpt(2), gg, lds[1], gu, lds[2], h, lds[3], None)
+
+    assert back(gu=at(11) + 78, lds=(40, 80, 80, 40)) == E and "overlap" in _lib.last_error()
+    assert back(gu=at(11) + 82, lds=(40, 80, 80, 40)) == E          # wraps into the next row's first column
+    assert back(gg=None) == E and back(h=at(11)) == E and back(lds=(40, 39, 40, 40)) == E and back(h=at(0)) == E
+
+
+def wgrad(**kw):
+    a = _lib.MuonWgrad()
+    a.grad_y, a.ld_grad_y, a.slots, a.outs, a.dtype = at(10), 24, 8, 24, BF16
+    a.ckpt = ckpt()
+    a.experts, a.out, a.out_dtype = 1, at(12), F32
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def run_wgrad(lib, a, ws=at(20), n=1 << 30):
+    return lib.muon_ckpt_wgrad(ctypes.byref(a), ws, n, None)
+
+
+def test_wgrad_refusals(lib):
+    cases = [
+        (dict(dtype=F32), U), (dict(out_dtype=9), U), (dict(slots=-1), E), (dict(outs=0), E), (dict(experts=0), E),
+        (dict(experts=2), E), (dict(slots=9), E), (dict(outs=(1 << 20) + 1, ld_grad_y=1 << 21), U), (dict(ckpt=ckpt(fmt=4)), U),
+        (dict(experts=65536, offsets=at(14)), U), (dict(ckpt=ckpt(cols=1 << 16, codes_ld=1 << 16, scales_ld=1 << 11), outs=1 << 16, ld_grad_y=1 << 16), U),
+    ]
+    for kw, status in cases:
+        assert run_wgrad(lib, wgrad(**kw)) == status, (kw, _lib.last_error())
+        assert lib.muon_ckpt_wgrad_workspace_size(ctypes.byref(wgrad(**kw))) == 0
+    for kw in (dict(grad_y=None), dict(ld_grad_y=23), dict(out=None), dict(out=at(12) + 2), dict(out=at(10) + 16), dict(out=at(0)),
+               dict(offsets=at(12) + 8), dict(rows_of=at(12) + 4 * 24 * 40 - 4), dict(grad_y=at(10) + 1)):
+        assert run_wgrad(lib, wgrad(**kw)) == E, (kw, _lib.last_error())
+        assert lib.muon_ckpt_wgrad_workspace_size(ctypes.byref(wgrad(**kw))) > 0          # sizes ignore pointers
+    assert run_wgrad(lib, wgrad(), ws=None) == E and run_wgrad(lib, wgrad(), ws=at(20) + 8) == E
+    assert run_wgrad(lib, wgrad(), ws=at(12)) == E
+    assert lib.muon_ckpt_wgrad(None, at(20), 1 << 20, None) == E
+    long = wgrad(slots=4096, ckpt=ckpt(rows=4096))
+    need = lib.muon_ckpt_wgrad_workspace_size(ctypes.byref(long))
+    assert need > 256 and need % 256 == 0
+    assert run_wgrad(lib, long, n=need - 1) == SMALL
+
+
+def routing(**kw):
+    a = _lib.MuonRouting()
+    a.logits, a.ld_logits, a.tokens, a.dtype, a.experts, a.top_k = at(10), 16, 9, BF16, 16, 4
+    a.groups = a.top_groups = 1
+    a.group_top, a.scale = 2, 1.0
+    a.expert_ids, a.weights = at(11), at(12)
+    a.counts, a.offsets, a.order, a.rows = at(13), at(14), at(15), at(16)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def test_routing_refusals(lib):
+    shape = [
+        (dict(dtype=3), U), (dict(score=2), E), (dict(tokens=-1), E), (dict(experts=0), E), (dict(top_k=0), E), (dict(top_k=17), E),
+        (dict(experts=1025, ld_logits=1025), U), (dict(experts=512, ld_logits=512, top_k=65), U), (dict(tokens=1 << 29), U), (dict(scale=math.nan), E),
+        (dict(logits=None), E), (dict(ld_logits=15), E), (dict(groups=3), E), (dict(groups=0), E), (dict(groups=4, top_groups=5), E),
+        (dict(groups=4, top_groups=0), E), (dict(group_top=3), E), (dict(groups=8, top_groups=1), E),
+        (dict(experts=256, ld_logits=256, groups=128, top_groups=64), U), (dict(order=None), E), (dict(counts=None), E),
+        (dict(counts=None, offsets=None, order=None, rows=None, load=at(18)), E), (dict(expert_ids=None), E), (dict(weights=None), E),
+        (dict(load=at(18) + 4), E),
+    ]
+    for kw, status in shape:
+        assert lib.muon_route(ctypes.byref(routing(**kw)), at(20), 1 << 30, None) == status, (kw, _lib.last_error())
+        assert lib.muon_route_workspace_size(ctypes.byref(routing(**kw))) == 0
+    for kw in (dict(expert_ids=at(10) + 2), dict(weights=at(11) + 4 * 35), dict(rows=at(15)), dict(bias=at(12)), dict(token_mask=at(13)), dict(load=at(16))):
+        assert lib.muon_route(ctypes.byref(routing(**kw)), at(20), 1 << 30, None) == E, kw
+        assert "overlap" in _lib.last_error()
+    need = lib.muon_route_workspace_size(ctypes.byref(routing()))
+    assert need > 0
+    assert lib.muon_route(ctypes.byref(routing()), at(20), need - 1, None) == SMALL
+    assert lib.muon_route(ctypes.byref(routing()), None, need, None) == E and lib.muon_route(None, at(20), need, None) == E
+    none = dict(counts=None, offsets=None, order=None, rows=None)
+    assert lib.muon_route(ctypes.byref(routing(tokens=0, logits=None, expert_ids=None, weights=None, **none)), at(20), 256, None) == OK
+
+
+def test_route_backward_and_balance_refusals(lib):
+    def back(dw=at(17), g=at(18), ld=16, **kw):
+        return lib.muon_route_backward(ctypes.byref(routing(**kw)), dw, g, ld, None)
+
+    assert back(dw=None) == E and back(g=None) == E and back(ld=15) == E and back(expert_ids=None) == E and back(g=at(10)) == E
+    assert back(g=at(17)) == E and back(top_k=17) == E and back(dtype=4) == U and back(scale=math.inf) == E
+    assert back(tokens=0, logits=None, expert_ids=None, dw=None, g=None) == OK
+
+    def balance(bias=at(0), counts=at(1), size=4, layers=2, experts=8, rate=0.1):
+        return lib.muon_balance_step(bias, counts, size, layers, experts, rate, None)
+
+    assert balance(bias=None) == E and balance(counts=None) == E and balance(size=2) == U and balance(layers=-1) == E
+    assert balance(experts=0) == E and balance(rate=math.nan) == E and balance(counts=at(0) + 32) == E and balance(counts=at(1) + 2) == E
+    assert balance(layers=1 << 40) == U and balance(layers=0, bias=None, counts=None) == OK
+
+
+def test_python_refusals_without_a_gpu():
+    x = torch.ones(4, 64)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        nsm.checkpoint_pack(x)
+    with pytest.raises(TypeError, match="torch.Tensor"):
+        nsm.checkpoint_pack([1.0])
+    with pytest.raises(TypeError, match="Checkpoint"):
+        nsm.checkpoint_unpack(x)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        nsm.Checkpoint(torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8), 64)
+    with pytest.raises(ValueError, match="format"):
+        nsm.Checkpoint(x, x, 64, "fp8")
+    with pytest.raises(ValueError, match="GPU tensor"):
+        nsm.route(x, 2)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        nsm.balance_step(torch.zeros(4), torch.zeros(4, dtype=torch.int32), rate=0.1)
+
+
+STUBS = r'''
+#include "train_kernels.h"
+#include <string>
+namespace muon {
+static thread_local std::string last;
+muon_status record_error(muon_status s, const char *msg) { last = msg ? msg : ""; return s; }
+hipError_t launch_ckpt_pack(const CkptArgs &, int, int, hipStream_t) { return hipErrorNotSupported; }
+hipError_t launch_ckpt_unpack(const CkptArgs &, int, int, hipStream_t) { return hipErrorNotSupported; }
+hipError_t launch_ckpt_swiglu(const CkptArgs &, int, int, hipStream_t) { return hipErrorNotSupported; }
+hipError_t launch_ckpt_swiglu_backward(const CkptArgs &, int, int, hipStream_t) { return hipErrorNotSupported; }
+hipError_t launch_wgrad(const WgradArgs &, int, int, hipStream_t) { return hipErrorNotSupported; }
+hipError_t launch_wgrad_join(const WgradArgs &, hipStream_t) { return hipErrorNotSupported; }
+hipError_t launch_route(const RouteArgs &, int, hipStream_t) { return hipErrorNotSupported; }
+hipError_t launch_route_backward(const RouteArgs &, int, hipStream_t) { return hipErrorNotSupported; }
+hipError_t launch_balance(float *, const void *, int, int64_t, int, float, hipStream_t) { return hipErrorNotSupported; }
+}
+'''
+
+DRIVER = r'''
+#include <stdint.h>
+#include <stdio.h>
+#include <stdlib.h>
+#include <string.h>
+#include "muon.h"
+#include "train_kernels.h"
+static uintptr_t at(int i) { return ((uintptr_t)1 << 40) + (uintptr_t)i * ((uintptr_t)1 << 36); }
+int main() {
+  int bad = 0;
+  // the division by multiplication, over divisors and their multiples' edges
+  for (uint32_t d = 1; d < 40000; d += 1 + d / 7) {
+    const muon::FastDiv f = muon::make_fastdiv(d);
+    for (uint32_t q = 0; q < 60; ++q) {
+      const uint32_t n0 = (uint32_t)(((uint64_t)q * 36600000u) / d * d);
+      for (int k = -1; k <= 1; ++k) {
+        const uint32_t n = n0 + (uint32_t)k;
+        if (n >= 0x80000000u) continue;
+        const uint32_t got = ((uint32_t)(((uint64_t)f.mul * n) >> 32) + n) >> f.shift;
+        if (got != n / d) bad++;
+      }
+    }
+  }
+  int64_t sizes[] = {0, 1, 31, 32, 33, 255, 4096, 70001, (int64_t)1 << 20};
+  for (int64_t rows : sizes)
+    for (int64_t cols : sizes) {
+      muon_ckpt c;
+      memset(&c, 0, sizeof c);
+      c.codes = (uint8_t *)at(0); c.scales = (uint8_t *)at(4); c.rows = rows; c.cols = cols;
+      c.codes_ld = (cols + 15) / 16 * 16; c.scales_ld = (cols + 31) / 32;
+      for (int t = 0; t < 3; ++t) {
+        muon_ckpt_pack((void *)at(8), cols, (muon_dtype)t, &c, 0);
+        muon_ckpt_unpack(&c, (void *)at(8), cols, (muon_dtype)t, 0);
+        muon_ckpt d = c;
+        d.codes = (uint8_t *)at(12); d.scales = (uint8_t *)at(16);
+        muon_ckpt_swiglu((void *)at(20), cols, (void *)at(24), cols, (muon_dtype)t, (void *)at(28), cols, &c, &d, 0);
+        muon_ckpt_swiglu_backward((void *)at(20), cols, (muon_dtype)t, &c, &d, (void *)at(24), 2 * cols,
+                                  (void *)(at(24) + (t ? 2 : 4) * cols), 2 * cols, 0, 0, 0);
+        for (int64_t outs : sizes) {
+          muon_wgrad w;
+          memset(&w, 0, sizeof w);
+          w.grad_y = (void *)at(40); w.ld_grad_y = outs; w.slots = rows; w.outs = outs; w.dtype = (muon_dtype)t; w.ckpt = c;
+          w.experts = 1; w.out = (void *)at(60); w.out_dtype = (muon_dtype)t;
+          size_t n = muon_ckpt_wgrad_workspace_size(&w);
+          if (n && muon_ckpt_wgrad(&w, (void *)at(300), n, 0) == MUON_OK) bad++;
+          if (n && muon_ckpt_wgrad(&w, (void *)at(300), n - 1, 0) != MUON_ERR_WORKSPACE_TOO_SMALL) bad++;
+        }
+      }
+    }
+  for (int64_t tokens : sizes)
+    for (int experts = 1; experts <= 1024; experts = experts * 3 + 1)
+      for (int k = 1; k <= 64 && k <= experts; k *= 2) {
+        muon_routing r;
+        memset(&r, 0, sizeof r);
+        r.logits = (void *)at(0); r.ld_logits = experts; r.tokens = tokens; r.experts = experts; r.top_k = k; r.groups = r.top_groups = 1;
+        r.group_top = 2; r.scale = 1; r.expert_ids = (int32_t *)at(4); r.weights = (float *)at(8); r.counts = (int32_t *)at(12);
+        r.offsets = (int32_t *)at(16); r.order = (int32_t *)at(20); r.rows = (int32_t *)at(24); r.load = (int64_t *)at(28);
+        size_t n = muon_route_workspace_size(&r);
+        if (!n || muon_route(&r, (void *)at(32), n, 0) != MUON_ERR_HIP) bad++;
+        const muon_status s = muon_route_backward(&r, (float *)at(40), (void *)at(44), experts, 0);
+        if (s != (tokens ? MUON_ERR_HIP : MUON_OK)) bad++;
+      }
+  printf("%s %d\n", bad ? "FAIL" : "OK", bad);
+  return bad != 0;
+}
+'''
+
+
+def test_training_host_code_under_asan_ubsan(tmp_path):
+    gxx = shutil.which("g++")
+    if gxx is None or not os.path.exists("/opt/rocm/include/hip/hip_runtime.h"):
+        pytest.skip("g++ or the ROCm headers are missing")
+    (tmp_path / "stubs.cpp").write_text(STUBS)
+    (tmp_path / "driver.cpp").write_text(DRIVER)
+    flags = ["-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined", "-fno-omit-frame-pointer",
+             "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", "-I" + INCLUDE, "-I" + CSRC]
+    exe = str(tmp_path / "driver")
+    r = subprocess.run([gxx] + flags + [os.path.join(CSRC, "train_host.cpp"), str(tmp_path / "stubs.cpp"), str(tmp_path / "driver.cpp"),
+                       "-L/opt/rocm/lib", "-lamdhip64", "-Wl,-rpath,/opt/rocm/lib", "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
+    env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:abort_on_error=0:verify_asan_link_order=0", UBSAN_OPTIONS="print_stacktrace=1")
+    r = subprocess.run([exe], capture_output=True, text=True, env=env, timeout=120)
+    assert r.returncode == 0 and "OK 0" in r.stdout, (r.stdout[-2000:], r.stderr[-4000:])
