@@ -127,6 +127,8 @@ muon_status check_pair(const muon_ckpt *a, const muon_ckpt *b) {
 // ------------------------------------------------------------------ wgrad
 
 struct WgradPlan {
+  int wide = 0;            // WgradArgs::wide
+  int64_t tiles_n = 0, tiles_d = 0;
   int splits = 1;
   int64_t split_len = 0;
   size_t bytes = 256;
@@ -148,18 +150,39 @@ muon_status check_wgrad(const muon_wgrad *a) {
   return MUON_OK;
 }
 
-// A single matrix of few output tiles has its token range cut into parts
-// that are joined in order afterwards, so that the parts' blocks fill the chip.
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tiles and parts.  The parts depend on shapes alone, so neither the workspace
+// size nor the order of a sum (steps of 32 tokens, parts in order) changes
+// with an operand's address or stride.
 WgradPlan plan_wgrad(const muon_wgrad *a) {
   WgradPlan p;
-  const int64_t tiles = ((a->outs + kWgradTile - 1) / kWgradTile) * ((a->ckpt.cols + kWgradTile - 1) / kWgradTile);
+  const int64_t N = a->outs, D = a->ckpt.cols;
+  const int64_t waste1 = ceil_div(N, 256) * 256 * ceil_div(D, 128) * 128, waste2 = ceil_div(N, 128) * 128 * ceil_div(D, 256) * 256;
+  if (N > 64 && D > 64) p.wide = waste1 <= waste2 ? 1 : 2;
+  const int64_t tiles = ceil_div(N, p.wide == 1 ? 256 : 128) * ceil_div(D, p.wide == 2 ? 256 : 128);
+  // what the wide tiles' DMA and 32-bit offsets need
+  const bool aligned = N % 8 == 0 && a->ld_grad_y % 8 == 0 && (((uintptr_t)a->grad_y) & 15) == 0 && a->ld_grad_y <= (1 << 24) &&
+                       a->ckpt.codes_ld <= (1 << 27) && a->ckpt.scales_ld <= (1 << 27) && a->ckpt.rows > 0;
+  if (!aligned) p.wide = 0;
+  p.tiles_n = ceil_div(N, p.wide == 1 ? 256 : 128);
+  p.tiles_d = ceil_div(D, p.wide == 2 ? 256 : 128);
   if (a->offsets || a->slots == 0) return p;
-  const int64_t want = std::min<int64_t>((512 + tiles - 1) / tiles, a->slots / 256);
-  if (want <= 1) return p;
-  const int64_t len = ((a->slots + want - 1) / want + kWgradK - 1) / kWgradK * kWgradK;
-  p.splits = (int)((a->slots + len - 1) / len);
-  p.split_len = len;
-  if (p.splits > 1) p.bytes = align256((size_t)p.splits * (size_t)(a->outs * a->ckpt.cols) * 4);
+  // Few output tiles leave most of the chip idle: the token range is cut into
+  // parts whose fp32 results are joined in order.  Each part count's time is
+  // estimated (512 blocks run at once, a step of 32 tokens takes 0.5 us, ten
+  // more fill and empty a block; partials pass memory twice at 4.5 TB/s, the
+  // join costs a launch) and the best is taken.
+  double best = 1e30;
+  for (int64_t s = 1; s <= 64; ++s) {
+    if (s > 1 && a->slots / s < 64) break;
+    const int64_t len = ceil_div(ceil_div(a->slots, s), kWgradK) * kWgradK;
+    if (ceil_div(a->slots, len) != s) continue;
+    double t = (double)ceil_div(tiles * s, 512) * ((double)(len / kWgradK) + 10) * 0.5e-6;
+    if (s > 1) t += (double)(s * N * D) * 8.0 / 4.5e12 + 4e-6;
+    if (t < best) best = t, p.splits = (int)s, p.split_len = len;
+  }
+  if (p.splits > 1) p.bytes = align256((size_t)p.splits * (size_t)(N * D) * 4);
   return p;
 }
 
@@ -349,8 +372,9 @@ muon_status muon_ckpt_wgrad(const muon_wgrad *args, void *workspace, size_t work
   a.experts = w.experts;
   a.splits = p.splits;
   a.split_len = p.split_len;
-  a.tiles_n = (int32_t)((w.outs + kWgradTile - 1) / kWgradTile);
-  a.tiles_d = (int32_t)((w.ckpt.cols + kWgradTile - 1) / kWgradTile);
+  a.tiles_n = (int32_t)p.tiles_n;
+  a.tiles_d = (int32_t)p.tiles_d;
+  a.wide = p.wide;
   a.out_dtype = (int32_t)w.out_dtype;
   a.accumulate = w.accumulate != 0;
   a.transposed = w.transposed != 0;

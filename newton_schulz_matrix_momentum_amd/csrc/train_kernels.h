@@ -75,6 +75,7 @@ struct WgradArgs {
   int32_t out_dtype;
   int32_t accumulate;
   int32_t transposed;
+  int32_t wide;            // 0: 128 x 128 tiles; 1: 256 outs x 128 columns; 2: 128 x 256
 };
 constexpr int kWgradTile = 128;
 constexpr int kWgradK = 32;
