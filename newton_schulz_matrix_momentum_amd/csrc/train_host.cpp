@@ -129,7 +129,9 @@ muon_status check_pair(const muon_ckpt *a, const muon_ckpt *b) {
 struct WgradPlan {
   int wide = 0;            // WgradArgs::wide
   int64_t tiles_n = 0, tiles_d = 0;
-  int splits = 1;
+  int blocks = 0;          // wide: blocks of the launch, a multiple of 8
+  bool segments = false;   // wide, one matrix: runs of steps, partials joined
+  int splits = 1;          // else: parts of the token range
   int64_t split_len = 0;
   size_t bytes = 256;
 };
@@ -152,37 +154,57 @@ muon_status check_wgrad(const muon_wgrad *a) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tiles and parts.  The parts depend on shapes alone, so neither the workspace
-// size nor the order of a sum (steps of 32 tokens, parts in order) changes
-// with an operand's address or stride.
-WgradPlan plan_wgrad(const muon_wgrad *a) {
-  WgradPlan p;
+constexpr int kWideBlocks = 512;               // two a CU
+constexpr int64_t kWidePart = int64_t(256) * 128 * 4;
+
+// 128 x 128 tiles of one matrix: the token range is cut into parts so that the
+// blocks fill the chip; the parts are joined in order.
+void plan_parts(const muon_wgrad *a, WgradPlan &p) {
+  const int64_t want = std::min<int64_t>(ceil_div(512, p.tiles_n * p.tiles_d), a->slots / 256);
+  if (a->offsets || want <= 1) return;
+  p.split_len = ceil_div(ceil_div(a->slots, want), kWgradK) * kWgradK;
+  p.splits = (int)ceil_div(a->slots, p.split_len);
+  if (p.splits > 1) p.bytes = (size_t)p.splits * (size_t)(a->outs * a->ckpt.cols) * 4;
+}
+
+// Wide tiles.  One matrix: each number of blocks' time is estimated (512 run
+// at once; a pair of steps takes 0.9 us, the fill and the stores as long as
+// eight; partials pass memory twice at 4.5 TB/s and their join costs a launch)
+// and the best is taken.
+bool plan_wide(const muon_wgrad *a, WgradPlan &p) {
   const int64_t N = a->outs, D = a->ckpt.cols;
+  if (N <= 64 || D <= 64 || N % 8 != 0 || a->slots == 0 || a->ckpt.rows == 0) return false;
   const int64_t waste1 = ceil_div(N, 256) * 256 * ceil_div(D, 128) * 128, waste2 = ceil_div(N, 128) * 128 * ceil_div(D, 256) * 256;
-  if (N > 64 && D > 64) p.wide = waste1 <= waste2 ? 1 : 2;
-  const int64_t tiles = ceil_div(N, p.wide == 1 ? 256 : 128) * ceil_div(D, p.wide == 2 ? 256 : 128);
-  // what the wide tiles' DMA and 32-bit offsets need
-  const bool aligned = N % 8 == 0 && a->ld_grad_y % 8 == 0 && (((uintptr_t)a->grad_y) & 15) == 0 && a->ld_grad_y <= (1 << 24) &&
-                       a->ckpt.codes_ld <= (1 << 27) && a->ckpt.scales_ld <= (1 << 27) && a->ckpt.rows > 0;
-  if (!aligned) p.wide = 0;
+  p.wide = waste1 <= waste2 ? 1 : 2;
   p.tiles_n = ceil_div(N, p.wide == 1 ? 256 : 128);
   p.tiles_d = ceil_div(D, p.wide == 2 ? 256 : 128);
-  if (a->offsets || a->slots == 0) return p;
-  // Few output tiles leave most of the chip idle: the token range is cut into
-  // parts whose fp32 results are joined in order.  Each part count's time is
-  // estimated (512 blocks run at once, a step of 32 tokens takes 0.5 us, ten
-  // more fill and empty a block; partials pass memory twice at 4.5 TB/s, the
-  // join costs a launch) and the best is taken.
+  const int64_t tiles = p.tiles_n * p.tiles_d, pairs = ceil_div(a->slots, 2 * kWgradK);
+  p.blocks = kWideBlocks;
+  if (tiles * a->experts >= (int64_t(1) << 30) || tiles * pairs >= (int64_t(1) << 30)) return false;
+  if (a->offsets) return true;
+  p.segments = true;
   double best = 1e30;
-  for (int64_t s = 1; s <= 64; ++s) {
-    if (s > 1 && a->slots / s < 64) break;
-    const int64_t len = ceil_div(ceil_div(a->slots, s), kWgradK) * kWgradK;
-    if (ceil_div(a->slots, len) != s) continue;
-    double t = (double)ceil_div(tiles * s, 512) * ((double)(len / kWgradK) + 10) * 0.5e-6;
-    if (s > 1) t += (double)(s * N * D) * 8.0 / 4.5e12 + 4e-6;
-    if (t < best) best = t, p.splits = (int)s, p.split_len = len;
+  for (int64_t b = 8; b <= kWideBlocks; b += 8) {
+    const double t = ((double)ceil_div(tiles * pairs, b) + 8) * 0.9e-6 + (tiles % b ? (double)(b * kWidePart) * 2 / 4.5e12 + 4e-6 : 0.0);
+    if (t < best) best = t, p.blocks = (int)b;
   }
-  if (p.splits > 1) p.bytes = align256((size_t)p.splits * (size_t)(N * D) * 4);
+  p.bytes = (size_t)(2 * p.blocks) * (size_t)kWidePart;
+  return true;
+}
+
+WgradPlan plan_wgrad(const muon_wgrad *a) {
+  WgradPlan wide, p;
+  const bool fits = plan_wide(a, wide);
+  p.tiles_n = ceil_div(a->outs, kWgradTile);
+  p.tiles_d = ceil_div(a->ckpt.cols, kWgradTile);
+  plan_parts(a, p);
+  // the size covers both, whatever grad_y's address and strides allow
+  const size_t bytes = align256(std::max(fits ? wide.bytes : 0, p.bytes));
+  const bool aligned = a->ld_grad_y % 8 == 0 && (((uintptr_t)a->grad_y) & 15) == 0 && a->ld_grad_y <= (1 << 24) &&
+                       a->ckpt.codes_ld <= (1 << 25) && a->ckpt.scales_ld <= (1 << 25) &&
+                       (!a->rows_of || a->ckpt.rows * std::max(a->ckpt.codes_ld, a->ckpt.scales_ld) < (int64_t(1) << 32) - 1);
+  if (fits && aligned) p = wide;
+  p.bytes = bytes;
   return p;
 }
 
@@ -375,6 +397,15 @@ muon_status muon_ckpt_wgrad(const muon_wgrad *args, void *workspace, size_t work
   a.tiles_n = (int32_t)p.tiles_n;
   a.tiles_d = (int32_t)p.tiles_d;
   a.wide = p.wide;
+  a.segments = p.segments;
+  a.blocks = p.blocks;
+  if (p.wide) {
+    const int64_t tiles = p.tiles_n * p.tiles_d, pairs = ceil_div(w.slots, 2 * kWgradK);
+    a.total_pairs = (int32_t)(tiles * pairs);
+    a.per_tile = make_fastdiv((uint32_t)pairs);
+    a.tiles = make_fastdiv((uint32_t)tiles);
+    a.div_d = make_fastdiv((uint32_t)p.tiles_d);
+  }
   a.out_dtype = (int32_t)w.out_dtype;
   a.accumulate = w.accumulate != 0;
   a.transposed = w.transposed != 0;

@@ -39,9 +39,31 @@ __device__ __forceinline__ uint32_t pair(float a, float b) {
   }
 }
 
+// two values rounded to a 16-bit type as an output
+template <int DT>
+__device__ __forceinline__ uint32_t raw_pair(float a, float b) {
+  const f32x2v v = {a, b};
+  if constexpr (DT == kF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+  else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
 // 16 codes with one scale as 16-bit operands
 template <int DT, int FMT>
 __device__ __forceinline__ void decode16(const u32x4 &w, uint32_t b, u32x4 &lo, u32x4 &hi) {
+  if constexpr (DT == kBF16 && FMT == MUON_E4M3) {
+    // one conversion a pair; 2^(b - 127) as it stands in a float's exponent
+    // (255 there makes every code NaN; bytes under 3, which pack never
+    // writes, flush the products below 2^-126 to zero)
+    const float e = __uint_as_float(b << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t p = __builtin_bit_cast(uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], e, false));
+      const uint32_t q = __builtin_bit_cast(uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], e, true));
+      if (i < 2) lo[2 * i] = p, lo[2 * i + 1] = q;
+      else hi[2 * (i - 2)] = p, hi[2 * (i - 2) + 1] = q;
+    }
+    return;
+  }
   const float s = scale_of(b);
   float v[4];
 #pragma unroll
@@ -235,16 +257,29 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradArgs args) {
     }
 }
 
+// Output row and first of 4 consecutive columns of accumulator (i, k) of a wide
+// tile: the MFMA's rows (4 consecutive a lane) are contiguous in the output.
+template <bool TRANS, int BN, int BD>
+__device__ __forceinline__ void place(int n0, int d0, int wave, int lane, int i, int k, int &r, int &c) {
+  constexpr bool LONG_Y = BN == 256;
+  const int il = 16 * i + (TRANS == LONG_Y ? 4 * (lane >> 4) : (lane & 15));
+  const int is = 16 * k + (TRANS == LONG_Y ? (lane & 15) : 4 * (lane >> 4));
+  const int n = n0 + (wave >> 1) * (BN / 2) + (LONG_Y ? il : is), d = d0 + (wave & 1) * (BD / 2) + (LONG_Y ? is : il);
+  r = TRANS ? d : n;
+  c = TRANS ? n : d;
+}
+
 // ---------------------------------------------------------------------------
-// Large products: BN outs x BD columns per block (256 x 128 or 128 x 256), four
-// waves of half the sides, two blocks a CU, so that one block's prologue and
-// stores run beside the other's products.
+// Large products: BN outs x BD columns per tile (256 x 128 or 128 x 256), four
+// waves of half the sides, two blocks a CU.
 //
-// A step is 32 tokens.  dy goes global -> LDS by DMA into a ring of kRing
-// stages, issued kRing steps ahead; x^ passes through registers (codes loaded
-// four steps ahead, decoded and written two ahead) into a ring of two.  Every
-// step issues the same memory operations (rows outside the expert come from a
-// page of zeros, or are zeroed while they are decoded), so the wait for a
+// A step is 32 tokens.  dy goes global -> LDS by DMA into a ring of four
+// stages, issued four steps ahead; x^ passes through registers (codes loaded
+// four steps ahead, decoded and written two ahead) into a ring of two.  Blocks
+// stay and walk a list of pieces (a tile and a range of its tokens); the loads
+// run ahead across pieces, so only a block's first piece waits for memory.
+// Every step issues the same number of loads (past a piece's last row, and for
+// slots that are left out, buffer loads return zeros), so the wait for a
 // stage's DMA is a constant count.
 //
 // A wave holds the short operand's four fragments and half of the long
@@ -258,6 +293,106 @@ constexpr uint64_t kRowBits = 0x0101010101010101ull;
 #define MUON_WGRAD_VMCNT(n) (0x0F70 | ((n) & 15) | (((n) >> 4) << 14))   // s_waitcnt vmcnt(n) alone
 
 template <int I> struct IntC { static constexpr int value = I; };
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+
+// bytes [0, bytes) from p as a buffer: reads behind them give zeros
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void *)uniform((int64_t)p), 0, uniform((int)bytes), 0x00020000);
+}
+
+// A block's pieces.  Parts of a single matrix (args.segments): the matrix's
+// tiles x steps are cut into one run a block.  Experts: whole tiles; each XCD
+// takes one run of them, of about an eighth of the work, and its blocks take
+// the run's tiles in turn, so that they share the operand panels in its L2.
+struct Piece {
+  int n0, d0;
+  int part;                // expert
+  int lo;                  // first slot
+  int rows;                // slots
+  int steps;               // even, >= 2: the last ones may be empty
+  int slot;                // -1: whole, to the matrix; else the partial's place
+};
+
+struct Walk {
+  int first, end;          // segments: pairs of steps; else tiles of this block's XCD
+  int step;                // stride between this block's tiles; segments: the block
+};
+
+// n / d for a wave-uniform n
+__device__ __forceinline__ int quotient(const FastDiv &f, int n) { return (int)((__umulhi(f.mul, (uint32_t)n) + (uint32_t)n) >> f.shift); }
+
+template <int BN, int BD>
+__device__ __forceinline__ bool piece_at(const WgradArgs &args, const Walk &w, int k, Piece &p) {
+  int tile;
+  if (args.segments) {
+    const int ppt = (int)args.per_tile.d;
+    tile = quotient(args.per_tile, w.first) + k;
+    const int base = tile * ppt;
+    const int s0 = max(w.first - base, 0), s1 = min(w.end - base, ppt);
+    if (s0 >= s1) return false;
+    p.part = 0;
+    p.lo = s0 * 2 * kWgradK;
+    p.steps = (s1 - s0) * 2;
+    p.rows = min((int)args.slots - p.lo, p.steps * kWgradK);
+    p.slot = s1 - s0 == ppt ? -1 : 2 * w.step + (k > 0);
+  } else {
+    const int t = w.first + k * w.step;
+    if (t >= w.end) return false;
+    p.part = quotient(args.tiles, t);
+    tile = t - p.part * (int)args.tiles.d;
+    int64_t lo, hi;
+    slot_range(args, p.part, lo, hi);
+    p.lo = (int)lo;
+    p.rows = (int)(hi - lo);
+    p.steps = max((p.rows + 2 * kWgradK - 1) / (2 * kWgradK), 1) * 2;
+    p.slot = -1;
+  }
+  const int tn = quotient(args.div_d, tile);
+  p.n0 = tn * BN;
+  p.d0 = (tile - tn * args.tiles_d) * BD;
+  return true;
+}
+
+// First tile of XCD x: where the running sum of the tiles' steps (and what a
+// tile costs besides) reaches x eighths of the whole.
+__device__ __forceinline__ int tile_of_share(const WgradArgs &args, int x, int lane) {
+  const int tiles = (int)args.tiles.d;
+  if (x == 8) return args.experts * tiles;
+  auto cost = [&](int e) -> int {
+    if (e >= args.experts) return 0;
+    int64_t lo, hi;
+    slot_range(args, e, lo, hi);
+    return ((int)(hi - lo) + 2 * kWgradK - 1) / (2 * kWgradK) + 4;        // pairs of steps
+  };
+  int64_t total = 0;
+  for (int base = 0; base < args.experts; base += 64) {
+    int64_t v = cost(base + lane);
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    total += v;
+  }
+  const int64_t target = total * tiles * x / 8;
+  int64_t before = 0;
+  for (int base = 0; base < args.experts; base += 64) {
+    const int v = cost(base + lane);
+    int64_t sum = v;
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t u = __shfl_up(sum, o, 64);
+      if (lane >= o) sum += u;
+    }
+    const int64_t start = (before + sum - v) * tiles, stop = (before + sum) * tiles;
+    const uint64_t here = __ballot(target >= start && target < stop);
+    if (here) {
+      const int at = (base + lane) * tiles + (v ? (int)((float)(target - start) / (float)v) : 0);
+      return min(__builtin_amdgcn_readlane(at, __ffsll((unsigned long long)here) - 1), args.experts * tiles);
+    }
+    before += __shfl(sum, 63, 64);
+  }
+  return args.experts * tiles;
+}
 
 template <int DT, int FMT, bool TRANS, bool GATHER, int BN, int BD>
 __global__ __launch_bounds__(kThreads, 2) void wgrad_wide_kernel(WgradArgs args) {
@@ -289,248 +424,387 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_wide_kernel(WgradArgs args)
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave >> 1, wd = wave & 1;
-  // consecutive blocks go to the XCDs in turn: each XCD walks one contiguous
-  // run of tiles, whose operand panels its L2 then holds
-  const int total = (int)gridDim.x, per = total / 8, rem = total % 8, xcd = blockIdx.x % 8;
-  int tile = (xcd < rem ? xcd * (per + 1) : rem * (per + 1) + (xcd - rem) * per) + blockIdx.x / 8;
-  const int tiles = args.tiles_n * args.tiles_d;
-  const int part = tile / tiles;                             // expert, or part of the token range
-  tile -= part * tiles;
-  const int e = args.splits > 1 ? 0 : part;
-  int64_t lo, hi;
-  slot_range(args, e, lo, hi);
-  if (args.splits > 1) {
-    lo += part * args.split_len;
-    hi = min(hi, lo + args.split_len);
+  // blocks go to the XCDs in turn
+  const int xcd = blockIdx.x % 8, per = (int)gridDim.x / 8;
+  Walk walk;
+  if (args.segments) {
+    const int b = xcd * per + blockIdx.x / 8;
+    walk.first = (int)((int64_t)args.total_pairs * b / args.blocks);
+    walk.end = (int)((int64_t)args.total_pairs * (b + 1) / args.blocks);
+    walk.step = b;
+  } else {
+    walk.first = tile_of_share(args, xcd, lane) + blockIdx.x / 8;
+    walk.end = tile_of_share(args, xcd + 1, lane);
+    walk.step = per;
   }
-  const int n0 = (tile / args.tiles_d) * BN, d0 = (tile % args.tiles_d) * BD;
-  const int steps = (int)((max(hi - lo, (int64_t)0) + kWgradK - 1) / kWgradK);
+  walk.first = __builtin_amdgcn_readfirstlane(walk.first);
+  walk.end = __builtin_amdgcn_readfirstlane(walk.end);
 
-  f32x4 acc[8][4] = {};
-  if (steps > 0) {
-    const int64_t last = hi - 1;
-    // dy: wave w moves rows 8 w .. 8 w + 7 of a stage.  A step's rows are a
-    // buffer that ends with the expert's last row, so rows behind it read as
-    // zeros, as do slots that are left out (an offset past any end).  Columns
-    // past outs (whole chunks: outs is a multiple of 8) read the last ones.
-    constexpr int RPI = 64 / LPR;                            // rows of a DMA instruction
-    constexpr int NO = RPI == 2 ? 2 : 1;                     // lane offsets that differ between instructions
-    const uint32_t y_pitch = (uint32_t)args.ld_dy * 2;
-    uint32_t y_off[NO];
+  // dy: wave w moves rows 8 w .. 8 w + 7 of a stage.  A step's rows are a
+  // buffer that ends with the piece's last row.  Columns past outs (whole
+  // chunks: outs is a multiple of 8) read the last ones.
+  constexpr int RPI = 64 / LPR;                              // rows of a DMA instruction
+  constexpr int NO = RPI == 2 ? 2 : 1;                       // lane offsets that differ between instructions
+  const uint32_t y_pitch = (uint32_t)args.ld_dy * 2, y_tail = (uint32_t)args.outs * 2;
+  uint32_t y_off[NO];
+  const char *y_at = nullptr;
+  // x^: rows 8 w + lane / 8 (one chunk), or 8 w + lane / 16 and 4 further (two)
+  const int x_row = wave * 8 + lane / CPR, x_chunk = lane % CPR;
+  const uint32_t c_pitch = (uint32_t)args.codes_ld, s_pitch = (uint32_t)args.scales_ld;
+  uint32_t c_off = 0, s_off = 0;
+  const uint8_t *c_at = nullptr, *s_at = nullptr;
+  int left = 0, steps_left = 0, next_piece = 0;              // of the piece being loaded
+  const int32_t *l_at = nullptr;                             // GATHER: the list, two steps further ahead
+  int l_left = 0, l_steps = 0, l_piece = 0;
+
+  // the loads go on to the next piece
+  auto enter = [&]() {
+    Piece p;
+    if (!piece_at<BN, BD>(args, walk, next_piece++, p)) {
+      left = 0;
+      steps_left = 1 << 30;
+      return;
+    }
+    left = uniform(p.rows);
+    steps_left = uniform(p.steps);
+    p.lo = uniform(p.lo);
+    y_at = (const char *)args.dy + (int64_t)p.lo * args.ld_dy * 2;
 #pragma unroll
     for (int o = 0; o < NO; ++o) {
       const int r = wave * 8 + o * RPI + lane / LPR, q = lane % LPR, c = (((q >> 1) ^ key(r)) << 1) | (q & 1);
-      y_off[o] = (uint32_t)(wave * 8 + lane / LPR) * y_pitch + (uint32_t)min(n0 + c * 8, args.outs - 8) * 2;
+      y_off[o] = (uint32_t)(wave * 8 + lane / LPR) * y_pitch + (uint32_t)min(p.n0 + c * 8, args.outs - 8) * 2;
     }
-    auto dma = [&](int step, auto sc, uint64_t valid) {
-      const int64_t row = lo + (int64_t)step * kWgradK;
-      const int64_t left = min(max(hi - row, (int64_t)0), (int64_t)kWgradK);
-      const __amdgpu_buffer_rsrc_t rows = __builtin_amdgcn_make_buffer_rsrc(
-          (void *)((const char *)args.dy + row * args.ld_dy * 2), 0, left > 0 ? (int)((uint32_t)(left - 1) * y_pitch + (uint32_t)args.outs * 2) : 0, 0x00020000);
-#pragma unroll
-      for (int j = 0; j < ND; ++j) {
-        uint32_t off = y_off[j % NO];
-        if constexpr (GATHER) {
-          if (valid != kRowBits && !((valid >> (8 * (j * RPI + lane / LPR))) & 1)) off = 0x80000000u;
-        }
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rows, (__attribute__((address_space(3))) void *)(ybuf(sc) + (wave * 8 * YROW + j * 1024)), 16,
-                                                 (int)off, (int)((uint32_t)(j * RPI) * y_pitch), 0, 0);
-      }
-    };
-    // x^: rows 8 w + lane / 8 (one chunk), or 8 w + lane / 16 and 4 further (two)
-    const int x_sub = lane / CPR, x_row = wave * 8 + x_sub, x_chunk = lane % CPR;
-    const uint32_t x_col = (uint32_t)min(d0 + x_chunk * 16, (args.cols - 1) & ~15);
-    struct Saved {
-      u32x4 w[NX];
-      uint32_t b[NX];
-      uint64_t in;           // bit 8 k: row 8 w + k is in (of kRowBits)
-    } saved[2];
-    // GATHER: a stage's checkpoint rows are loaded two steps before they are
-    // checked (check: -1 where the slot is left out) and used
-    int row[2][NX];
-    auto find = [&](int step, int (&out)[NX]) {
-#pragma unroll
-      for (int x = 0; x < NX; ++x) out[x] = args.rows_of[min(lo + (int64_t)step * kWgradK + x_row + 4 * x, last)];
-    };
-    auto check = [&](int step, int (&r)[NX]) -> uint64_t {
-      uint64_t m[NX];
-#pragma unroll
-      for (int x = 0; x < NX; ++x) {
-        const bool in = lo + (int64_t)step * kWgradK + x_row + 4 * x < hi && r[x] >= 0 && r[x] < args.ckpt_rows;
-        r[x] = in ? r[x] : -1;
-        m[x] = __ballot(in);
-      }
-      // a row's lanes start at 8 k (one chunk a thread) or at 16 k (two)
-      if constexpr (NX == 1) return m[0] & kRowBits;
-      uint64_t v = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v |= ((m[0] >> (16 * k)) & 1) << (8 * k) | ((m[NX - 1] >> (16 * k)) & 1) << (8 * (k + 4));
-      return v;
-    };
-    auto fetch = [&](int step, Saved &s, const int (&from)[NX], uint64_t valid) {
-      const int64_t base = lo + (int64_t)step * kWgradK + wave * 8;
-      const int64_t first = min(base, last);                 // wave-uniform
-      s.in = valid;
-#pragma unroll
-      for (int x = 0; x < NX; ++x) {
-        if constexpr (GATHER) {
-          const int64_t r = max(from[x], 0);
-          s.w[x] = *(const u32x4 *)(args.codes + r * args.codes_ld + x_col);
-          s.b[x] = args.scales[r * args.scales_ld + x_col / kCkptBlock];
-        } else {
-          const uint32_t k = min((uint32_t)(x_sub + 4 * x), (uint32_t)min(last - first, (int64_t)7));
-          s.w[x] = *(const u32x4 *)(args.codes + first * args.codes_ld + (k * (uint32_t)args.codes_ld + x_col));
-          s.b[x] = *(args.scales + first * args.scales_ld + (k * (uint32_t)args.scales_ld + x_col / kCkptBlock));
-        }
-      }
-    };
-    // validity of a stage's 8 rows of this wave without a list
-    auto tail = [&](int step) -> uint64_t {
-      const int64_t left = hi - (lo + (int64_t)step * kWgradK + wave * 8);
-      return left >= 8 ? kRowBits : left <= 0 ? 0ull : ((1ull << (8 * left)) - 1) & kRowBits;
-    };
-    auto stage = [&](auto sc, const Saved &s) {
-#pragma unroll
-      for (int x = 0; x < NX; ++x) {
-        u32x4 a, b, w = s.w[x];
-        uint32_t sb = s.b[x];
-        if (s.in != kRowBits && !((s.in >> (8 * (x_sub + 4 * x))) & 1)) w = u32x4{}, sb = 127;
-        decode16<DT, FMT>(w, sb, a, b);
-        const int r = x_row + 4 * x;
-        const int o = r * XROW + ((x_chunk ^ key(r)) * 32);
-        *(u32x4 *)(xbuf(sc) + o) = a;
-        *(u32x4 *)(xbuf(sc) + (o + 16)) = b;
-      }
-    };
-    // Fragment c of a stage (16 columns): tokens 8 g .. 8 g + 7 of the lane's
-    // column, from rows r0 and r0 + 4 (their keys are equal).  Its chunk's
-    // place differs from fragment 0's by c in the three bits of the key, so
-    // the offset is one exclusive or.  The base passes through an empty asm
-    // each step: kept apart for each fragment, the offsets would cost 12
-    // registers, and as a chain of sums they lose the stage they point into.
-    constexpr int LROW = LONG_Y ? YROW : XROW, SROW = LONG_Y ? XROW : YROW;
-    const int r0 = 8 * (lane >> 4) + ((lane & 15) >> 2), lc = (LONG_Y ? wn : wd) * 8, sc0 = (LONG_Y ? wd : wn) * 4;
-    int at_long = r0 * LROW + ((lc ^ key(r0)) * 32) + (lane & 3) * 8;
-    int at_short = r0 * SROW + ((sc0 ^ key(r0)) * 32) + (lane & 3) * 8;
-    auto fresh = [](int &o) { asm volatile("" : "+v"(o)); };
-    auto frag = [&](const char *t, int o, int half) {
-      const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4 *)(t + o));
-      const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4 *)(t + o + half));
-      const uint2 a = __builtin_bit_cast(uint2, x), b = __builtin_bit_cast(uint2, y);
-      return u32x4{a.x, a.y, b.x, b.y};
-    };
-    auto frag_long = [&](auto sc, int i) {
-      if constexpr (LONG_Y) return frag(ybuf(sc), at_long ^ (i * 32), 4 * YROW);
-      else return frag(xbuf(sc), at_long ^ (i * 32), 4 * XROW);
-    };
-    auto frag_short = [&](auto sc, int i) {
-      if constexpr (LONG_Y) return frag(xbuf(sc), at_short ^ (i * 32), 4 * XROW);
-      else return frag(ybuf(sc), at_short ^ (i * 32), 4 * YROW);
-    };
-    u32x4 fs[4], fl[4], fh[4];
-    auto column = [&](int base, const u32x4 (&f)[4], int k) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (TRANS == LONG_Y) mma<DT>(f[i], fs[k], acc[base + i][k]);    // rows: the long operand's index
-        else mma<DT>(fs[k], f[i], acc[base + i][k]);
-      }
-    };
-
-    // fill: steps 0 .. 3 in the steady order (dma, codes), steps 0 and 1 decoded
+    const uint32_t col = (uint32_t)min(p.d0 + x_chunk * 16, (args.cols - 1) & ~15);
     if constexpr (GATHER) {
-      find(0, row[0]);
-      find(1, row[1]);
+      c_off = col;
+      s_off = col / kCkptBlock;
+    } else {
+      c_off = (uint32_t)x_row * c_pitch + col;
+      s_off = (uint32_t)x_row * s_pitch + col / kCkptBlock;
+      c_at = args.codes + (int64_t)p.lo * args.codes_ld;
+      s_at = args.scales + (int64_t)p.lo * args.scales_ld;
     }
-    auto fill = [&](auto sc) {
-      constexpr int i = decltype(sc)::value;
-      const uint64_t v = GATHER ? check(i, row[i & 1]) : tail(i);
-      dma(i, sc, v);
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (i >= 2) stage(sc, saved[i & 1]);
-      __builtin_amdgcn_sched_barrier(0);
-      fetch(i, saved[i & 1], row[i & 1], v);
-      if constexpr (GATHER) find(i + 2, row[i & 1]);
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    fill(IntC<0>{});
-    fill(IntC<1>{});
-    fill(IntC<2>{});
-    fill(IntC<3>{});
-    // row[] now holds steps 4 and 5
-    __builtin_amdgcn_s_waitcnt(0);
+  };
+  auto enter_list = [&]() {
+    Piece p;
+    if (!piece_at<BN, BD>(args, walk, l_piece++, p)) {
+      l_left = 0;
+      l_steps = 1 << 30;
+      return;
+    }
+    l_left = uniform(p.rows);
+    l_steps = uniform(p.steps);
+    l_at = args.rows_of + uniform(p.lo);
+  };
+  struct Saved {
+    u32x4 w[NX];
+    uint32_t b[NX];
+  } saved[2];
+  // GATHER: a stage's checkpoint rows are loaded two steps before they are used
+  int row[2][NX];
+  auto find = [&](int (&out)[NX]) {
+    const __amdgpu_buffer_rsrc_t b = buffer(l_at, (uint32_t)min(max(l_left, 0), kWgradK) * 4);
+#pragma unroll
+    for (int x = 0; x < NX; ++x) out[x] = __builtin_amdgcn_raw_buffer_load_b32(b, (x_row + 4 * x) * 4, 0, 0);
+    l_at += kWgradK;
+    l_left -= kWgradK;
+  };
+  // GATHER: rows that are left out become -1; bit 8 k of the result: row 8 w + k is in
+  auto check = [&](int (&r)[NX]) -> uint64_t {
+    uint64_t m[NX];
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+      const bool in = x_row + 4 * x < left && r[x] >= 0 && r[x] < args.ckpt_rows;
+      r[x] = in ? r[x] : -1;
+      m[x] = __ballot(in);
+    }
+    // a row's lanes start at 8 k (one chunk a thread) or at 16 k (two)
+    if constexpr (NX == 1) return m[0] & kRowBits;
+    uint64_t v = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v |= ((m[0] >> (16 * k)) & 1) << (8 * k) | ((m[NX - 1] >> (16 * k)) & 1) << (8 * (k + 4));
+    return v;
+  };
+  auto dma = [&](auto sc, uint64_t valid) {
+    const __amdgpu_buffer_rsrc_t b = buffer(y_at, left > 0 ? (uint32_t)(min(left, kWgradK) - 1) * y_pitch + y_tail : 0u);
+#pragma unroll
+    for (int j = 0; j < ND; ++j) {
+      uint32_t off = y_off[j % NO] + (uint32_t)(j * RPI) * y_pitch;
+      if constexpr (GATHER) {
+        if (valid != kRowBits && !((valid >> (8 * (j * RPI + lane / LPR))) & 1)) off = 0x80000000u;    // past any end
+      }
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void *)(ybuf(sc) + (wave * 8 * YROW + j * 1024)), 16,
+                                               (int)off, 0, 0, 0);
+    }
+  };
+  auto fetch = [&](Saved &s, const int (&from)[NX]) {
+    if constexpr (GATHER) {
+      const __amdgpu_buffer_rsrc_t c = buffer(args.codes, (uint32_t)args.ckpt_rows * c_pitch), t = buffer(args.scales, (uint32_t)args.ckpt_rows * s_pitch);
+#pragma unroll
+      for (int x = 0; x < NX; ++x) {
+        const uint32_t r = (uint32_t)from[x];
+        s.w[x] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(c, from[x] < 0 ? -1 : (int)(r * c_pitch + c_off), 0, 0));
+        s.b[x] = __builtin_amdgcn_raw_buffer_load_b8(t, from[x] < 0 ? -1 : (int)(r * s_pitch + s_off), 0, 0);
+      }
+    } else {
+      const uint32_t n = (uint32_t)min(max(left, 0), kWgradK);
+      const __amdgpu_buffer_rsrc_t c = buffer(c_at, n * c_pitch), t = buffer(s_at, n * s_pitch);
+#pragma unroll
+      for (int x = 0; x < NX; ++x) {
+        s.w[x] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(c, (int)(c_off + 4 * x * c_pitch), 0, 0));
+        s.b[x] = __builtin_amdgcn_raw_buffer_load_b8(t, (int)(s_off + 4 * x * s_pitch), 0, 0);
+      }
+    }
+  };
+  auto advance = [&]() {
+    y_at += (int64_t)kWgradK * y_pitch;
+    if constexpr (!GATHER) {
+      c_at += (int64_t)kWgradK * args.codes_ld;
+      s_at += (int64_t)kWgradK * args.scales_ld;
+    }
+    left -= kWgradK;
+  };
+  // after every second step: pieces have even numbers of steps, and so have
+  // the distances that loads run ahead
+  auto turn = [&]() {
+    if ((steps_left -= 2) == 0) enter();
+    if constexpr (GATHER) {
+      if ((l_steps -= 2) == 0) enter_list();
+    }
+  };
+  struct Decoded {
+    u32x4 a[NX], b[NX];
+  };
+  auto decode = [&](const Saved &s, Decoded &d) {
+#pragma unroll
+    for (int x = 0; x < NX; ++x) decode16<DT, FMT>(s.w[x], s.b[x], d.a[x], d.b[x]);
+  };
+  auto stage = [&](auto sc, const Decoded &d) {
+#pragma unroll
+    for (int x = 0; x < NX; ++x) {
+      const int r = x_row + 4 * x, o = r * XROW + ((x_chunk ^ key(r)) * 32);
+      *(u32x4 *)(xbuf(sc) + o) = d.a[x];
+      *(u32x4 *)(xbuf(sc) + (o + 16)) = d.b[x];
+    }
+  };
+  // Fragment c of a stage (16 columns): tokens 8 g .. 8 g + 7 of the lane's
+  // column, from rows r0 and r0 + 4 (their keys are equal).  Its chunk's
+  // place differs from fragment 0's by c in the three bits of the key, so
+  // the offset is one exclusive or.  The base passes through an empty asm
+  // each step: kept apart for each fragment, the offsets would cost 12
+  // registers, and as a chain of sums they lose the stage they point into.
+  constexpr int LROW = LONG_Y ? YROW : XROW, SROW = LONG_Y ? XROW : YROW;
+  const int r0 = 8 * (lane >> 4) + ((lane & 15) >> 2), lc = (LONG_Y ? wn : wd) * 8, sc0 = (LONG_Y ? wd : wn) * 4;
+  int at_long = r0 * LROW + ((lc ^ key(r0)) * 32) + (lane & 3) * 8;
+  int at_short = r0 * SROW + ((sc0 ^ key(r0)) * 32) + (lane & 3) * 8;
+  auto fresh = [](int &o) { asm volatile("" : "+v"(o)); };
+  auto frag = [&](const char *t, int o, int half) {
+    const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4 *)(t + o));
+    const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4 *)(t + o + half));
+    const uint2 a = __builtin_bit_cast(uint2, x), b = __builtin_bit_cast(uint2, y);
+    return u32x4{a.x, a.y, b.x, b.y};
+  };
+  auto frag_long = [&](auto sc, int i) {
+    if constexpr (LONG_Y) return frag(ybuf(sc), at_long ^ (i * 32), 4 * YROW);
+    else return frag(xbuf(sc), at_long ^ (i * 32), 4 * XROW);
+  };
+  auto frag_short = [&](auto sc, int i) {
+    if constexpr (LONG_Y) return frag(xbuf(sc), at_short ^ (i * 32), 4 * XROW);
+    else return frag(ybuf(sc), at_short ^ (i * 32), 4 * YROW);
+  };
+  f32x4 acc[8][4] = {};
+  u32x4 fs[4], fl[4], fh[4];
+  auto column = [&](int base, const u32x4 (&f)[4], int k) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (TRANS == LONG_Y) mma<DT>(f[i], fs[k], acc[base + i][k]);    // rows: the long operand's index
+      else mma<DT>(fs[k], f[i], acc[base + i][k]);
+    }
+  };
+
+  Piece now;
+  if (!piece_at<BN, BD>(args, walk, 0, now)) return;
+  int piece = 0, remaining = now.steps;
+  if constexpr (GATHER) {
+    enter_list();
+    find(row[0]);
+    find(row[1]);
+    if ((l_steps -= 2) == 0) enter_list();
+  }
+  enter();
+  // fill: steps 0 .. 3 in the steady order (dma, codes), steps 0 and 1 decoded
+  auto fill = [&](auto sc) {
+    constexpr int i = decltype(sc)::value;
+    uint64_t v = 0;
+    if constexpr (GATHER) v = check(row[i & 1]);
+    dma(sc, v);
+    if constexpr (i >= 2) {
+      Decoded d;
+      decode(saved[i & 1], d);
+      stage(sc, d);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(saved[i & 1], row[i & 1]);
+    if constexpr (GATHER) find(row[i & 1]);
+    advance();
+    if constexpr (i & 1) turn();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  fill(IntC<0>{});
+  fill(IntC<1>{});
+  fill(IntC<2>{});
+  fill(IntC<3>{});
+  // steps 0 and 1 were decoded, so their dma, which was issued before their
+  // codes, has landed; row[] now holds steps 4 and 5
+  __builtin_amdgcn_s_waitcnt(0xC07F);         // lgkmcnt(0): the decoded rows are written
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) fs[k] = frag_short(IntC<0>{}, k), fl[k] = frag_long(IntC<0>{}, k);
+
+  // loads a wave has issued behind the DMA of stage i + 1 when step i waits for
+  // it: codes (and list) of step i + 1, and two steps of both; the older ones
+  // of those have to be there anyway
+  constexpr int BEHIND = 2 * ND + 2 * NX * (GATHER ? 3 : 2);
+  auto step = [&](auto sc) {
+    constexpr int S = decltype(sc)::value;
+    const IntC<S + 1> next;
+    Saved &s = saved[S & 1];
+    int (&r)[NX] = row[S & 1];
+    fresh(at_long);
+    fresh(at_short);
+    Decoded d;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) fh[k] = frag_long(sc, 4 + k);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) column(0, fl, k);
+    decode(s, d);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(MUON_WGRAD_VMCNT(BEHIND));
+    __builtin_amdgcn_s_waitcnt(0xC07F);       // lgkmcnt(0): stage i + 1's codes are written, stage i is in registers
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
+    uint64_t v = 0;
+    if constexpr (GATHER) v = check(r);
+    stage(sc, d);
+    dma(sc, v);
+    fetch(s, r);
+    if constexpr (GATHER) find(r);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) fs[k] = frag_short(IntC<0>{}, k), fl[k] = frag_long(IntC<0>{}, k);
-
-    auto step = [&](auto sc, int i) {
-      constexpr int S = decltype(sc)::value;                 // i % 4
-      const IntC<S + 1> next;
-      Saved &s = saved[S & 1];
-      int (&r)[NX] = row[S & 1];
-      fresh(at_long);
-      fresh(at_short);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) fh[k] = frag_long(sc, 4 + k);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) column(0, fl, k);
-      // stage i + 1: its dma has landed (behind it: three steps of codes and
-      // indices, two of dma; the newest of those may stay on their way), its
-      // codes are written; stage i is in registers
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(MUON_WGRAD_VMCNT(2 * ND + 2 * NX * (GATHER ? 3 : 2)));
-      __builtin_amdgcn_s_waitcnt(0xC07F);     // lgkmcnt(0)
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-      const uint64_t v = GATHER ? check(i + 4, r) : tail(i + 4);
-      dma(i + 4, sc, v);
-      __builtin_amdgcn_sched_barrier(0);
-      stage(sc, s);
-      __builtin_amdgcn_sched_barrier(0);
-      fetch(i + 4, s, r, v);
-      if constexpr (GATHER) find(i + 6, r);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) fl[k] = frag_long(next, k);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        column(4, fh, k);
-        fs[k] = frag_short(next, k);
-      }
-    };
-#pragma unroll 1
-    for (int i = 0;;) {
-      step(IntC<0>{}, i);
-      if (++i >= steps) break;
-      step(IntC<1>{}, i);
-      if (++i >= steps) break;
-      step(IntC<2>{}, i);
-      if (++i >= steps) break;
-      step(IntC<3>{}, i);
-      if (++i >= steps) break;
-    }
-    // nothing may still be on its way to LDS when the block's LDS is given on
-    __builtin_amdgcn_s_waitcnt(0);
-  }
-
-  const int rows = TRANS ? args.cols : args.outs, width = TRANS ? args.outs : args.cols;
-  const int64_t size = (int64_t)args.outs * args.cols;
-  const bool split = args.splits > 1;
-  const int ot = split ? (int)kF32 : args.out_dtype;
-  void *const out = split ? (void *)args.part : args.out;
-  const bool vec = (width & 3) == 0 && (((uintptr_t)out) & 15) == 0;
-  const int64_t first = (int64_t)part * size;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
+    for (int k = 0; k < 4; ++k) fl[k] = frag_long(next, k);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      // the MFMA's rows (4 consecutive a lane) are contiguous in the output
-      const int il = 16 * i + (TRANS == LONG_Y ? 4 * (lane >> 4) : (lane & 15));
-      const int is = 16 * k + (TRANS == LONG_Y ? (lane & 15) : 4 * (lane >> 4));
-      const int n = n0 + wn * (BN / 2) + (LONG_Y ? il : is), d = d0 + wd * (BD / 2) + (LONG_Y ? is : il);
-      const int r = TRANS ? d : n, c = TRANS ? n : d;
-      if (r < rows && c < width) put4_any(out, ot, first + (int64_t)r * width + c, min(width - c, 4), vec, !split && args.accumulate, acc[i][k]);
+      column(4, fh, k);
+      fs[k] = frag_short(next, k);
     }
+    __builtin_amdgcn_sched_barrier(0);
+    advance();
+    if constexpr (S & 1) turn();
+  };
+
+  // the piece is done: to the matrix or to its partial; false: it was the last
+  constexpr bool ROWS_LONG = TRANS == LONG_Y;                // the MFMA's rows index the long operand
+  const int rows = TRANS ? args.cols : args.outs, width = TRANS ? args.outs : args.cols;
+  const bool wide_store = !args.accumulate && (((uintptr_t)args.out) & 15) == 0 && (width & 7) == 0;
+  auto finish = [&]() -> bool {
+    if (now.slot >= 0) {
+      float *dst = args.part + ((int64_t)now.slot * 32 * kThreads + tid) * 4;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) *(f32x4 *)(dst + (i * 4 + k) * kThreads * 4) = acc[i][k];
+    } else if (wide_store) {
+      // 16 bytes a lane, 64 of a row an instruction: fp32 as it lies; of a
+      // 16-bit type, neighbouring 16-lane rows swap halves of two neighbouring
+      // fragments, which leaves each lane 8 consecutive columns
+      constexpr int NF = ROWS_LONG ? 8 : 4, NR = ROWS_LONG ? 4 : 8;      // fragments along a row, and across rows
+      int r, c;
+      place<TRANS, BN, BD>(now.n0, now.d0, wave, lane, 0, 0, r, c);
+      const int64_t at = ((int64_t)now.part * args.outs * args.cols + (int64_t)r * width);
+#pragma unroll
+      for (int q = 0; q < NR; ++q) {
+        const bool in = r + 16 * q < rows;
+#pragma unroll
+        for (int f = 0; f < NF; f += 2) {
+          const f32x4 u = ROWS_LONG ? acc[f][q] : acc[q][f], v = ROWS_LONG ? acc[f + 1][q] : acc[q][f + 1];
+          if (args.out_dtype == kF32) {
+            float *p = (float *)args.out + at + (int64_t)(16 * q) * width + c + 16 * f;
+            if (in && c + 16 * f < width) *(f32x4 *)p = u;
+            if (in && c + 16 * f + 16 < width) *(f32x4 *)(p + 16) = v;
+          } else {
+            const bool bf = args.out_dtype == kBF16;
+            const uint32_t u0 = bf ? raw_pair<kBF16>(u[0], u[1]) : raw_pair<kF16>(u[0], u[1]), u1 = bf ? raw_pair<kBF16>(u[2], u[3]) : raw_pair<kF16>(u[2], u[3]);
+            const uint32_t v0 = bf ? raw_pair<kBF16>(v[0], v[1]) : raw_pair<kF16>(v[0], v[1]), v1 = bf ? raw_pair<kBF16>(v[2], v[3]) : raw_pair<kF16>(v[2], v[3]);
+            const auto s0 = __builtin_amdgcn_permlane16_swap(u0, v0, false, false), s1 = __builtin_amdgcn_permlane16_swap(u1, v1, false, false);
+            // even rows: columns 4 g .. 4 g + 7 of the first fragment, odd rows 4 (g - 1) .. of the second
+            const int cc = c + 16 * f + ((lane & 16) ? 12 : 0);
+            if (in && cc < width) *(u32x4 *)((uint16_t *)args.out + at + (int64_t)(16 * q) * width + cc) = u32x4{s0[0], s1[0], s0[1], s1[1]};
+          }
+        }
+      }
+    } else {
+      const int64_t first = (int64_t)now.part * args.outs * args.cols;
+      const bool vec = (width & 3) == 0 && (((uintptr_t)args.out) & 15) == 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          int r, c;
+          place<TRANS, BN, BD>(now.n0, now.d0, wave, lane, i, k, r, c);
+          if (r < rows && c < width) put4_any(args.out, args.out_dtype, first + (int64_t)r * width + c, min(width - c, 4), vec, args.accumulate, acc[i][k]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i][k] = f32x4{};
+    if (!piece_at<BN, BD>(args, walk, ++piece, now)) return false;
+    remaining = now.steps;
+    return true;
+  };
+  bool even = true;          // the ring stands at stage 0, not at stage 2
+#pragma unroll 1
+  for (;;) {
+    if (even) {
+      step(IntC<0>{});
+      step(IntC<1>{});
+      remaining -= 2;
+    }
+    if (!even || remaining > 0) {
+      step(IntC<2>{});
+      step(IntC<3>{});
+      remaining -= 2;
+      even = true;
+    } else {
+      even = false;
+    }
+    if (remaining == 0 && !finish()) break;
+  }
+  // nothing may still be on its way to LDS when the block's LDS is given on
+  __builtin_amdgcn_s_waitcnt(0);
+}
+
+// The tiles that were cut: their partials in the blocks' order, 4 values a thread.
+template <bool TRANS, int BN, int BD>
+__global__ __launch_bounds__(kThreads) void wgrad_wide_join_kernel(WgradArgs args) {
+  const int t = blockIdx.x / 32, f = blockIdx.x % 32, tid = threadIdx.x;
+  const int64_t ppt = args.per_tile.d, G = args.total_pairs, P = args.blocks;
+  const int64_t t0 = t * ppt, t1 = t0 + ppt;
+  int64_t b = t0 * P / G;                     // the block whose run holds the tile's first steps
+  while (G * (b + 1) / P <= t0) ++b;
+  while (G * b / P > t0) --b;
+  if (G * (b + 1) / P >= t1) return;          // one block had all of it
+  f32x4 v = {};
+  for (; b < P && G * b / P < t1; ++b) {
+    if (G * b / P == G * (b + 1) / P) continue;                  // an empty run
+    const int64_t slot = 2 * b + (G * b / P < t0);
+    v += *(const f32x4 *)(args.part + ((slot * 32 + f) * kThreads + tid) * 4);
+  }
+  const int rows = TRANS ? args.cols : args.outs, width = TRANS ? args.outs : args.cols;
+  int r, c;
+  place<TRANS, BN, BD>(t / args.tiles_d * BN, t % args.tiles_d * BD, tid >> 6, tid & 63, f / 4, f % 4, r, c);
+  if (r < rows && c < width)
+    put4_any(args.out, args.out_dtype, (int64_t)r * width + c, min(width - c, 4), (width & 3) == 0 && (((uintptr_t)args.out) & 15) == 0, args.accumulate, v);
 }
 
 // out = (out +) the sum of the parts, in their order
@@ -558,7 +832,7 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(WgradArgs args) {
 
 template <int DT, int FMT>
 hipError_t launch_wide(const WgradArgs &args, hipStream_t s) {
-  const dim3 g((unsigned)(args.tiles_n * args.tiles_d * (args.splits > 1 ? args.splits : args.experts))), b(kThreads);
+  const dim3 g((unsigned)args.blocks), b(kThreads);
 #define MUON_WIDE(TRANS, GATHER)                                                                                             \
   if (args.wide == 1) hipLaunchKernelGGL((wgrad_wide_kernel<DT, FMT, TRANS, GATHER, 256, 128>), g, b, 0, s, args);           \
   else hipLaunchKernelGGL((wgrad_wide_kernel<DT, FMT, TRANS, GATHER, 128, 256>), g, b, 0, s, args)
@@ -567,6 +841,13 @@ hipError_t launch_wide(const WgradArgs &args, hipStream_t s) {
   else if (args.rows_of) MUON_WIDE(false, true);
   else MUON_WIDE(false, false);
 #undef MUON_WIDE
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !args.segments || args.blocks <= 1) return e;
+  const dim3 j((unsigned)(args.tiles_n * args.tiles_d * 32));
+  if (args.transposed && args.wide == 1) hipLaunchKernelGGL((wgrad_wide_join_kernel<true, 256, 128>), j, b, 0, s, args);
+  else if (args.transposed) hipLaunchKernelGGL((wgrad_wide_join_kernel<true, 128, 256>), j, b, 0, s, args);
+  else if (args.wide == 1) hipLaunchKernelGGL((wgrad_wide_join_kernel<false, 256, 128>), j, b, 0, s, args);
+  else hipLaunchKernelGGL((wgrad_wide_join_kernel<false, 128, 256>), j, b, 0, s, args);
   return hipGetLastError();
 }
 

@@ -230,7 +230,10 @@ def test_wgrad(nsm, tokens, outs, cols, dtype, fmt, out_dtype, transposed):
     assert got.dtype == DT[out_dtype]
     near(got, want, tol, "dW")
     again = nsm.checkpoint_wgrad(strided(dy.cuda(), outs + 1), c, out_dtype=DT[out_dtype], transposed=transposed)
-    assert torch.equal(again, got)                                   # strides change nothing, and runs are bitwise equal
+    # another stride may take another order of sums: both are within tol of the
+    # exact value, so they are within 2 tol of each other; runs are bitwise equal
+    near(again, want, tol, "dW strided")
+    assert torch.equal(got, nsm.checkpoint_wgrad(dy.cuda(), c, out_dtype=DT[out_dtype], transposed=transposed))
     base = activations(*got.shape, out_dtype, 9).cuda()
     total = to64(base) + want
     acc = nsm.checkpoint_wgrad(dy.cuda(), c, out=base, transposed=transposed, accumulate=True)
