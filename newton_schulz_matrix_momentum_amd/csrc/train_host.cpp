@@ -129,9 +129,7 @@ muon_status check_pair(const muon_ckpt *a, const muon_ckpt *b) {
 struct WgradPlan {
   int wide = 0;            // WgradArgs::wide
   int64_t tiles_n = 0, tiles_d = 0;
-  int blocks = 0;          // wide: blocks of the launch, a multiple of 8
-  bool segments = false;   // wide, one matrix: runs of steps, partials joined
-  int splits = 1;          // else: parts of the token range
+  int splits = 1;          // parts of the token range
   int64_t split_len = 0;
   size_t bytes = 256;
 };
@@ -167,10 +165,11 @@ void plan_parts(const muon_wgrad *a, WgradPlan &p) {
   if (p.splits > 1) p.bytes = (size_t)p.splits * (size_t)(a->outs * a->ckpt.cols) * 4;
 }
 
-// Wide tiles.  One matrix: each number of blocks' time is estimated (512 run
-// at once; a pair of steps takes 0.9 us, the fill and the stores as long as
-// eight; partials pass memory twice at 4.5 TB/s and their join costs a launch)
-// and the best is taken.
+// Wide tiles.  One matrix: each number of parts' time is estimated and the
+// best is taken.  A round of 512 pieces takes 1.0 us a step, one of at most
+// 256 (a block alone on its CU) 0.6; filling a block and storing a piece take
+// ten steps more; partials pass memory twice at 4.5 TB/s and their join costs
+// a launch.
 bool plan_wide(const muon_wgrad *a, WgradPlan &p) {
   const int64_t N = a->outs, D = a->ckpt.cols;
   if (N <= 64 || D <= 64 || N % 8 != 0 || a->slots == 0 || a->ckpt.rows == 0) return false;
@@ -178,17 +177,20 @@ bool plan_wide(const muon_wgrad *a, WgradPlan &p) {
   p.wide = waste1 <= waste2 ? 1 : 2;
   p.tiles_n = ceil_div(N, p.wide == 1 ? 256 : 128);
   p.tiles_d = ceil_div(D, p.wide == 2 ? 256 : 128);
-  const int64_t tiles = p.tiles_n * p.tiles_d, pairs = ceil_div(a->slots, 2 * kWgradK);
-  p.blocks = kWideBlocks;
-  if (tiles * a->experts >= (int64_t(1) << 30) || tiles * pairs >= (int64_t(1) << 30)) return false;
+  const int64_t tiles = p.tiles_n * p.tiles_d;
+  if (tiles * std::max<int64_t>(a->experts, 64) >= (int64_t(1) << 30)) return false;
   if (a->offsets) return true;
-  p.segments = true;
   double best = 1e30;
-  for (int64_t b = 8; b <= kWideBlocks; b += 8) {
-    const double t = ((double)ceil_div(tiles * pairs, b) + 8) * 0.9e-6 + (tiles % b ? (double)(b * kWidePart) * 2 / 4.5e12 + 4e-6 : 0.0);
-    if (t < best) best = t, p.blocks = (int)b;
+  for (int64_t s = 1; s <= 64; ++s) {
+    const int64_t len = ceil_div(ceil_div(a->slots, s), 2 * kWgradK) * 2 * kWgradK;
+    if (ceil_div(a->slots, len) != s) continue;
+    const int64_t items = tiles * s, rounds = ceil_div(items, kWideBlocks);
+    const double per_step = items <= kWideBlocks / 2 ? 0.6e-6 : 1.0e-6;
+    double t = (double)rounds * ((double)(len / kWgradK) + 10) * per_step;
+    if (s > 1) t += (double)(items * kWidePart) * 2 / 4.5e12 + 4e-6;
+    if (t < best) best = t, p.splits = (int)s, p.split_len = len;
   }
-  p.bytes = (size_t)(2 * p.blocks) * (size_t)kWidePart;
+  if (p.splits > 1) p.bytes = (size_t)(p.splits * tiles) * (size_t)kWidePart;
   return true;
 }
 
@@ -397,12 +399,10 @@ muon_status muon_ckpt_wgrad(const muon_wgrad *args, void *workspace, size_t work
   a.tiles_n = (int32_t)p.tiles_n;
   a.tiles_d = (int32_t)p.tiles_d;
   a.wide = p.wide;
-  a.segments = p.segments;
-  a.blocks = p.blocks;
   if (p.wide) {
-    const int64_t tiles = p.tiles_n * p.tiles_d, pairs = ceil_div(w.slots, 2 * kWgradK);
-    a.total_pairs = (int32_t)(tiles * pairs);
-    a.per_tile = make_fastdiv((uint32_t)pairs);
+    const int64_t tiles = p.tiles_n * p.tiles_d;
+    a.items = (int32_t)(tiles * (p.splits > 1 ? p.splits : w.experts));
+    a.blocks = (int32_t)std::min<int64_t>((a.items + 7) / 8 * 8, kWideBlocks);
     a.tiles = make_fastdiv((uint32_t)tiles);
     a.div_d = make_fastdiv((uint32_t)p.tiles_d);
   }
@@ -410,7 +410,7 @@ muon_status muon_ckpt_wgrad(const muon_wgrad *args, void *workspace, size_t work
   a.accumulate = w.accumulate != 0;
   a.transposed = w.transposed != 0;
   hipError_t e = launch_wgrad(a, (int)w.dtype, (int)w.ckpt.format, (hipStream_t)stream);
-  if (e == hipSuccess && p.splits > 1) e = launch_wgrad_join(a, (hipStream_t)stream);
+  if (e == hipSuccess && !p.wide && p.splits > 1) e = launch_wgrad_join(a, (hipStream_t)stream);
   return launched(e, "muon_ckpt_wgrad");
 }
 

@@ -76,10 +76,8 @@ struct WgradArgs {
   int32_t accumulate;
   int32_t transposed;
   int32_t wide;            // 0: 128 x 128 tiles; 1: 256 outs x 128 columns; 2: 128 x 256
-  int32_t segments;        // wide: the steps of all tiles are cut into one run a block
-  int32_t blocks;          // wide: blocks of the launch
-  int32_t total_pairs;     // segments: pairs of steps of all tiles
-  FastDiv per_tile, tiles, div_d;   // by the pairs of a tile, the tiles of a matrix, tiles_d
+  int32_t blocks, items;   // wide: blocks of the launch; tiles x experts or parts, which the blocks take in turn
+  FastDiv tiles, div_d;    // wide: by the tiles of a matrix, and by tiles_d
 };
 constexpr int kWgradTile = 128;
 constexpr int kWgradK = 32;

@@ -304,10 +304,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t
   return __builtin_amdgcn_make_buffer_rsrc((void *)uniform((int64_t)p), 0, uniform((int)bytes), 0x00020000);
 }
 
-// A block's pieces.  Parts of a single matrix (args.segments): the matrix's
-// tiles x steps are cut into one run a block.  Experts: whole tiles; each XCD
-// takes one run of them, of about an eighth of the work, and its blocks take
-// the run's tiles in turn, so that they share the operand panels in its L2.
+// A block's pieces: whole tiles of one expert, or of one part of a single
+// matrix's tokens, taken in rounds by all blocks.  Blocks go to the 8 XCDs in
+// turn; each XCD takes an eighth of a round's run of pieces, neighbouring
+// tiles, which share operand panels in its L2.  Experts come largest first
+// (up to 64 of them): the pieces of a round are then about equally long, and
+// the last round's the shortest.
 struct Piece {
   int n0, d0;
   int part;                // expert
@@ -318,8 +320,8 @@ struct Piece {
 };
 
 struct Walk {
-  int first, end;          // segments: pairs of steps; else tiles of this block's XCD
-  int step;                // stride between this block's tiles; segments: the block
+  int rank;                // of expert `lane`, by size
+  int first;               // this block's place in a round
 };
 
 // n / d for a wave-uniform n
@@ -327,71 +329,45 @@ __device__ __forceinline__ int quotient(const FastDiv &f, int n) { return (int)(
 
 template <int BN, int BD>
 __device__ __forceinline__ bool piece_at(const WgradArgs &args, const Walk &w, int k, Piece &p) {
-  int tile;
-  if (args.segments) {
-    const int ppt = (int)args.per_tile.d;
-    tile = quotient(args.per_tile, w.first) + k;
-    const int base = tile * ppt;
-    const int s0 = max(w.first - base, 0), s1 = min(w.end - base, ppt);
-    if (s0 >= s1) return false;
+  const int t = w.first + k * args.blocks;
+  if (t >= args.items) return false;
+  const int part = quotient(args.tiles, t), tile = t - part * (int)args.tiles.d;
+  if (args.splits > 1) {
     p.part = 0;
-    p.lo = s0 * 2 * kWgradK;
-    p.steps = (s1 - s0) * 2;
-    p.rows = min((int)args.slots - p.lo, p.steps * kWgradK);
-    p.slot = s1 - s0 == ppt ? -1 : 2 * w.step + (k > 0);
+    p.lo = part * (int)args.split_len;
+    p.rows = min((int)args.slots - p.lo, (int)args.split_len);
+    p.slot = t;
   } else {
-    const int t = w.first + k * w.step;
-    if (t >= w.end) return false;
-    p.part = quotient(args.tiles, t);
-    tile = t - p.part * (int)args.tiles.d;
+    p.part = part;
+    if (args.offsets && args.experts <= 64) p.part = __ffsll((unsigned long long)__ballot(w.rank == part)) - 1;
     int64_t lo, hi;
     slot_range(args, p.part, lo, hi);
     p.lo = (int)lo;
     p.rows = (int)(hi - lo);
-    p.steps = max((p.rows + 2 * kWgradK - 1) / (2 * kWgradK), 1) * 2;
     p.slot = -1;
   }
+  p.steps = max((p.rows + 2 * kWgradK - 1) / (2 * kWgradK), 1) * 2;
   const int tn = quotient(args.div_d, tile);
   p.n0 = tn * BN;
   p.d0 = (tile - tn * args.tiles_d) * BD;
   return true;
 }
 
-// First tile of XCD x: where the running sum of the tiles' steps (and what a
-// tile costs besides) reaches x eighths of the whole.
-__device__ __forceinline__ int tile_of_share(const WgradArgs &args, int x, int lane) {
-  const int tiles = (int)args.tiles.d;
-  if (x == 8) return args.experts * tiles;
-  auto cost = [&](int e) -> int {
-    if (e >= args.experts) return 0;
+// Rank of expert `lane` by size, the lower index first among equals
+__device__ __forceinline__ int size_rank(const WgradArgs &args, int lane) {
+  if (!args.offsets || args.experts > 64) return 0;
+  int size = -1;
+  if (lane < args.experts) {
     int64_t lo, hi;
-    slot_range(args, e, lo, hi);
-    return ((int)(hi - lo) + 2 * kWgradK - 1) / (2 * kWgradK) + 4;        // pairs of steps
-  };
-  int64_t total = 0;
-  for (int base = 0; base < args.experts; base += 64) {
-    int64_t v = cost(base + lane);
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-    total += v;
+    slot_range(args, lane, lo, hi);
+    size = (int)(hi - lo);
   }
-  const int64_t target = total * tiles * x / 8;
-  int64_t before = 0;
-  for (int base = 0; base < args.experts; base += 64) {
-    const int v = cost(base + lane);
-    int64_t sum = v;
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t u = __shfl_up(sum, o, 64);
-      if (lane >= o) sum += u;
-    }
-    const int64_t start = (before + sum - v) * tiles, stop = (before + sum) * tiles;
-    const uint64_t here = __ballot(target >= start && target < stop);
-    if (here) {
-      const int at = (base + lane) * tiles + (v ? (int)((float)(target - start) / (float)v) : 0);
-      return min(__builtin_amdgcn_readlane(at, __ffsll((unsigned long long)here) - 1), args.experts * tiles);
-    }
-    before += __shfl(sum, 63, 64);
+  int rank = 0;
+  for (int i = 0; i < args.experts; ++i) {
+    const int other = __builtin_amdgcn_readlane(size, i);
+    rank += other > size || (other == size && i < lane) ? 1 : 0;
   }
-  return args.experts * tiles;
+  return lane < args.experts ? rank : -1;
 }
 
 template <int DT, int FMT, bool TRANS, bool GATHER, int BN, int BD>
@@ -424,21 +400,7 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_wide_kernel(WgradArgs args)
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave >> 1, wd = wave & 1;
-  // blocks go to the XCDs in turn
-  const int xcd = blockIdx.x % 8, per = (int)gridDim.x / 8;
-  Walk walk;
-  if (args.segments) {
-    const int b = xcd * per + blockIdx.x / 8;
-    walk.first = (int)((int64_t)args.total_pairs * b / args.blocks);
-    walk.end = (int)((int64_t)args.total_pairs * (b + 1) / args.blocks);
-    walk.step = b;
-  } else {
-    walk.first = tile_of_share(args, xcd, lane) + blockIdx.x / 8;
-    walk.end = tile_of_share(args, xcd + 1, lane);
-    walk.step = per;
-  }
-  walk.first = __builtin_amdgcn_readfirstlane(walk.first);
-  walk.end = __builtin_amdgcn_readfirstlane(walk.end);
+  const Walk walk = {size_rank(args, lane), (int)(blockIdx.x % 8) * (args.blocks / 8) + (int)(blockIdx.x / 8)};
 
   // dy: wave w moves rows 8 w .. 8 w + 7 of a stage.  A step's rows are a
   // buffer that ends with the piece's last row.  Columns past outs (whole
@@ -784,22 +746,13 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_wide_kernel(WgradArgs args)
   __builtin_amdgcn_s_waitcnt(0);
 }
 
-// The tiles that were cut: their partials in the blocks' order, 4 values a thread.
+// The parts' partials in their order, 4 values a thread.
 template <bool TRANS, int BN, int BD>
 __global__ __launch_bounds__(kThreads) void wgrad_wide_join_kernel(WgradArgs args) {
   const int t = blockIdx.x / 32, f = blockIdx.x % 32, tid = threadIdx.x;
-  const int64_t ppt = args.per_tile.d, G = args.total_pairs, P = args.blocks;
-  const int64_t t0 = t * ppt, t1 = t0 + ppt;
-  int64_t b = t0 * P / G;                     // the block whose run holds the tile's first steps
-  while (G * (b + 1) / P <= t0) ++b;
-  while (G * b / P > t0) --b;
-  if (G * (b + 1) / P >= t1) return;          // one block had all of it
   f32x4 v = {};
-  for (; b < P && G * b / P < t1; ++b) {
-    if (G * b / P == G * (b + 1) / P) continue;                  // an empty run
-    const int64_t slot = 2 * b + (G * b / P < t0);
-    v += *(const f32x4 *)(args.part + ((slot * 32 + f) * kThreads + tid) * 4);
-  }
+  for (int p = 0; p < args.splits; ++p)
+    v += *(const f32x4 *)(args.part + ((((int64_t)p * (int)args.tiles.d + t) * 32 + f) * kThreads + tid) * 4);
   const int rows = TRANS ? args.cols : args.outs, width = TRANS ? args.outs : args.cols;
   int r, c;
   place<TRANS, BN, BD>(t / args.tiles_d * BN, t % args.tiles_d * BD, tid >> 6, tid & 63, f / 4, f % 4, r, c);
@@ -807,7 +760,7 @@ __global__ __launch_bounds__(kThreads) void wgrad_wide_join_kernel(WgradArgs arg
     put4_any(args.out, args.out_dtype, (int64_t)r * width + c, min(width - c, 4), (width & 3) == 0 && (((uintptr_t)args.out) & 15) == 0, args.accumulate, v);
 }
 
-// out = (out +) the sum of the parts, in their order
+// 128 x 128 tiles: out = (out +) the sum of the parts, in their order
 __global__ __launch_bounds__(256) void wgrad_join_kernel(WgradArgs args) {
   const int64_t size = (int64_t)args.outs * args.cols;
   const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
@@ -842,7 +795,7 @@ hipError_t launch_wide(const WgradArgs &args, hipStream_t s) {
   else MUON_WIDE(false, false);
 #undef MUON_WIDE
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !args.segments || args.blocks <= 1) return e;
+  if (e != hipSuccess || args.splits <= 1) return e;
   const dim3 j((unsigned)(args.tiles_n * args.tiles_d * 32));
   if (args.transposed && args.wide == 1) hipLaunchKernelGGL((wgrad_wide_join_kernel<true, 256, 128>), j, b, 0, s, args);
   else if (args.transposed) hipLaunchKernelGGL((wgrad_wide_join_kernel<true, 128, 256>), j, b, 0, s, args);
