@@ -76,7 +76,8 @@ __device__ __forceinline__ void decode16(const u32x4 &w, uint32_t b, u32x4 &lo, 
 }
 
 // One expert's slots [lo, hi), read clamped to the list's length
-__device__ __forceinline__ void slot_range(const WgradArgs &args, int e, int64_t &lo, int64_t &hi) {
+template <typename Args>
+__device__ __forceinline__ void slot_range(const Args &args, int e, int64_t &lo, int64_t &hi) {
   if (args.offsets) {
     lo = min(max((int64_t)args.offsets[e], (int64_t)0), args.slots);
     hi = min(max((int64_t)args.offsets[e + 1], lo), args.slots);
@@ -325,13 +326,25 @@ struct Walk {
 };
 
 // n / d for a wave-uniform n
-__device__ __forceinline__ int quotient(const FastDiv &f, int n) { return (int)((__umulhi(f.mul, (uint32_t)n) + (uint32_t)n) >> f.shift); }
+__device__ __forceinline__ int quotient(uint32_t mul, uint32_t shift, int n) { return (int)((__umulhi(mul, (uint32_t)n) + (uint32_t)n) >> shift); }
+
+// The kernel's arguments, read again where they are used: what a piece's start
+// and end need would otherwise fill the scalar registers all along, and their
+// overflow the vector registers.  (The empty asm hides where the address is
+// from, so the loads are not moved ahead.)
+typedef const WgradArgs __attribute__((address_space(4))) FarArgs;
+__device__ __forceinline__ FarArgs &far_args() {
+  FarArgs *a = (FarArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(a));
+  return *a;
+}
 
 template <int BN, int BD>
-__device__ __forceinline__ bool piece_at(const WgradArgs &args, const Walk &w, int k, Piece &p) {
+__device__ __forceinline__ bool piece_at(const Walk &w, int k, Piece &p) {
+  FarArgs &args = far_args();
   const int t = w.first + k * args.blocks;
   if (t >= args.items) return false;
-  const int part = quotient(args.tiles, t), tile = t - part * (int)args.tiles.d;
+  const int part = quotient(args.tiles.mul, args.tiles.shift, t), tile = t - part * (int)args.tiles.d;
   if (args.splits > 1) {
     p.part = 0;
     p.lo = part * (int)args.split_len;
@@ -339,15 +352,15 @@ __device__ __forceinline__ bool piece_at(const WgradArgs &args, const Walk &w, i
     p.slot = t;
   } else {
     p.part = part;
-    if (args.offsets && args.experts <= 64) p.part = __ffsll((unsigned long long)__ballot(w.rank == part)) - 1;
+    if (args.offsets && args.experts <= 64) p.part = uniform(__ffsll((unsigned long long)__ballot(w.rank == part)) - 1);
     int64_t lo, hi;
     slot_range(args, p.part, lo, hi);
-    p.lo = (int)lo;
-    p.rows = (int)(hi - lo);
+    p.lo = uniform((int)lo);
+    p.rows = uniform((int)(hi - lo));
     p.slot = -1;
   }
   p.steps = max((p.rows + 2 * kWgradK - 1) / (2 * kWgradK), 1) * 2;
-  const int tn = quotient(args.div_d, tile);
+  const int tn = quotient(args.div_d.mul, args.div_d.shift, tile);
   p.n0 = tn * BN;
   p.d0 = (tile - tn * args.tiles_d) * BD;
   return true;
@@ -408,55 +421,57 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_wide_kernel(WgradArgs args)
   constexpr int RPI = 64 / LPR;                              // rows of a DMA instruction
   constexpr int NO = RPI == 2 ? 2 : 1;                       // lane offsets that differ between instructions
   const uint32_t y_pitch = (uint32_t)args.ld_dy * 2, y_tail = (uint32_t)args.outs * 2;
-  uint32_t y_off[NO];
-  const char *y_at = nullptr;
   // x^: rows 8 w + lane / 8 (one chunk), or 8 w + lane / 16 and 4 further (two)
   const int x_row = wave * 8 + lane / CPR, x_chunk = lane % CPR;
   const uint32_t c_pitch = (uint32_t)args.codes_ld, s_pitch = (uint32_t)args.scales_ld;
-  uint32_t c_off = 0, s_off = 0;
-  const uint8_t *c_at = nullptr, *s_at = nullptr;
-  int left = 0, steps_left = 0, next_piece = 0;              // of the piece being loaded
-  const int32_t *l_at = nullptr;                             // GATHER: the list, two steps further ahead
-  int l_left = 0, l_steps = 0, l_piece = 0;
-
-  // the loads go on to the next piece
-  auto enter = [&]() {
+  // what is loaded next: rows of a piece from here on, and this lane's offsets
+  struct Source {
+    const char *y;
+    const uint8_t *c, *s;
+    uint32_t yo[NO], co, so;
+    int left, steps;
+  } src = {};
+  // GATHER: the list, two steps further ahead
+  struct List {
+    const int32_t *at;
+    int left, steps;
+  } list = {};
+  int next_piece = 0, next_list = 0;
+  auto enter = [&](Source o) -> Source {
     Piece p;
-    if (!piece_at<BN, BD>(args, walk, next_piece++, p)) {
-      left = 0;
-      steps_left = 1 << 30;
-      return;
+    if (!piece_at<BN, BD>(walk, next_piece++, p)) {
+      o.left = 0;
+      o.steps = 1 << 30;
+      return o;
     }
-    left = uniform(p.rows);
-    steps_left = uniform(p.steps);
+    FarArgs &args = far_args();
+    o.left = uniform(p.rows);
+    o.steps = uniform(p.steps);
     p.lo = uniform(p.lo);
-    y_at = (const char *)args.dy + (int64_t)p.lo * args.ld_dy * 2;
+    o.y = (const char *)args.dy + (int64_t)p.lo * args.ld_dy * 2;
 #pragma unroll
-    for (int o = 0; o < NO; ++o) {
-      const int r = wave * 8 + o * RPI + lane / LPR, q = lane % LPR, c = (((q >> 1) ^ key(r)) << 1) | (q & 1);
-      y_off[o] = (uint32_t)(wave * 8 + lane / LPR) * y_pitch + (uint32_t)min(p.n0 + c * 8, args.outs - 8) * 2;
+    for (int k = 0; k < NO; ++k) {
+      const int r = wave * 8 + k * RPI + lane / LPR, q = lane % LPR, c = (((q >> 1) ^ key(r)) << 1) | (q & 1);
+      o.yo[k] = (uint32_t)(wave * 8 + lane / LPR) * y_pitch + (uint32_t)min(p.n0 + c * 8, args.outs - 8) * 2;
     }
     const uint32_t col = (uint32_t)min(p.d0 + x_chunk * 16, (args.cols - 1) & ~15);
-    if constexpr (GATHER) {
-      c_off = col;
-      s_off = col / kCkptBlock;
-    } else {
-      c_off = (uint32_t)x_row * c_pitch + col;
-      s_off = (uint32_t)x_row * s_pitch + col / kCkptBlock;
-      c_at = args.codes + (int64_t)p.lo * args.codes_ld;
-      s_at = args.scales + (int64_t)p.lo * args.scales_ld;
+    o.co = GATHER ? col : (uint32_t)x_row * c_pitch + col;
+    o.so = GATHER ? col / kCkptBlock : (uint32_t)x_row * s_pitch + col / kCkptBlock;
+    if constexpr (!GATHER) {
+      o.c = args.codes + (int64_t)p.lo * args.codes_ld;
+      o.s = args.scales + (int64_t)p.lo * args.scales_ld;
     }
+    return o;
   };
-  auto enter_list = [&]() {
+  auto enter_list = [&](List o) -> List {
     Piece p;
-    if (!piece_at<BN, BD>(args, walk, l_piece++, p)) {
-      l_left = 0;
-      l_steps = 1 << 30;
-      return;
+    if (!piece_at<BN, BD>(walk, next_list++, p)) {
+      o.left = 0;
+      o.steps = 1 << 30;
+      return o;
     }
-    l_left = uniform(p.rows);
-    l_steps = uniform(p.steps);
-    l_at = args.rows_of + uniform(p.lo);
+    FarArgs &args = far_args();
+    return List{args.rows_of + uniform(p.lo), uniform(p.rows), uniform(p.steps)};
   };
   struct Saved {
     u32x4 w[NX];
@@ -465,18 +480,18 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_wide_kernel(WgradArgs args)
   // GATHER: a stage's checkpoint rows are loaded two steps before they are used
   int row[2][NX];
   auto find = [&](int (&out)[NX]) {
-    const __amdgpu_buffer_rsrc_t b = buffer(l_at, (uint32_t)min(max(l_left, 0), kWgradK) * 4);
+    const __amdgpu_buffer_rsrc_t b = buffer(list.at, (uint32_t)min(max(list.left, 0), kWgradK) * 4);
 #pragma unroll
     for (int x = 0; x < NX; ++x) out[x] = __builtin_amdgcn_raw_buffer_load_b32(b, (x_row + 4 * x) * 4, 0, 0);
-    l_at += kWgradK;
-    l_left -= kWgradK;
+    list.at += kWgradK;
+    list.left -= kWgradK;
   };
   // GATHER: rows that are left out become -1; bit 8 k of the result: row 8 w + k is in
   auto check = [&](int (&r)[NX]) -> uint64_t {
     uint64_t m[NX];
 #pragma unroll
     for (int x = 0; x < NX; ++x) {
-      const bool in = x_row + 4 * x < left && r[x] >= 0 && r[x] < args.ckpt_rows;
+      const bool in = x_row + 4 * x < src.left && r[x] >= 0 && r[x] < args.ckpt_rows;
       r[x] = in ? r[x] : -1;
       m[x] = __ballot(in);
     }
@@ -488,10 +503,10 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_wide_kernel(WgradArgs args)
     return v;
   };
   auto dma = [&](auto sc, uint64_t valid) {
-    const __amdgpu_buffer_rsrc_t b = buffer(y_at, left > 0 ? (uint32_t)(min(left, kWgradK) - 1) * y_pitch + y_tail : 0u);
+    const __amdgpu_buffer_rsrc_t b = buffer(src.y, src.left > 0 ? (uint32_t)(min(src.left, kWgradK) - 1) * y_pitch + y_tail : 0u);
 #pragma unroll
     for (int j = 0; j < ND; ++j) {
-      uint32_t off = y_off[j % NO] + (uint32_t)(j * RPI) * y_pitch;
+      uint32_t off = src.yo[j % NO] + (uint32_t)(j * RPI) * y_pitch;
       if constexpr (GATHER) {
         if (valid != kRowBits && !((valid >> (8 * (j * RPI + lane / LPR))) & 1)) off = 0x80000000u;    // past any end
       }
@@ -505,35 +520,41 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_wide_kernel(WgradArgs args)
 #pragma unroll
       for (int x = 0; x < NX; ++x) {
         const uint32_t r = (uint32_t)from[x];
-        s.w[x] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(c, from[x] < 0 ? -1 : (int)(r * c_pitch + c_off), 0, 0));
-        s.b[x] = __builtin_amdgcn_raw_buffer_load_b8(t, from[x] < 0 ? -1 : (int)(r * s_pitch + s_off), 0, 0);
+        s.w[x] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(c, from[x] < 0 ? -1 : (int)(r * c_pitch + src.co), 0, 0));
+        s.b[x] = __builtin_amdgcn_raw_buffer_load_b8(t, from[x] < 0 ? -1 : (int)(r * s_pitch + src.so), 0, 0);
       }
     } else {
-      const uint32_t n = (uint32_t)min(max(left, 0), kWgradK);
-      const __amdgpu_buffer_rsrc_t c = buffer(c_at, n * c_pitch), t = buffer(s_at, n * s_pitch);
+      const uint32_t n = (uint32_t)min(max(src.left, 0), kWgradK);
+      const __amdgpu_buffer_rsrc_t c = buffer(src.c, n * c_pitch), t = buffer(src.s, n * s_pitch);
 #pragma unroll
       for (int x = 0; x < NX; ++x) {
-        s.w[x] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(c, (int)(c_off + 4 * x * c_pitch), 0, 0));
-        s.b[x] = __builtin_amdgcn_raw_buffer_load_b8(t, (int)(s_off + 4 * x * s_pitch), 0, 0);
+        s.w[x] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(c, (int)(src.co + 4 * x * c_pitch), 0, 0));
+        s.b[x] = __builtin_amdgcn_raw_buffer_load_b8(t, (int)(src.so + 4 * x * s_pitch), 0, 0);
       }
     }
   };
   auto advance = [&]() {
-    y_at += (int64_t)kWgradK * y_pitch;
+    src.y += (int64_t)kWgradK * y_pitch;
     if constexpr (!GATHER) {
-      c_at += (int64_t)kWgradK * args.codes_ld;
-      s_at += (int64_t)kWgradK * args.scales_ld;
+      src.c += (int64_t)kWgradK * c_pitch;
+      src.s += (int64_t)kWgradK * s_pitch;
     }
-    left -= kWgradK;
+    src.left -= kWgradK;
   };
   // after every second step: pieces have even numbers of steps, and so have
   // the distances that loads run ahead
   auto turn = [&]() {
-    if ((steps_left -= 2) == 0) enter();
+    src.steps = uniform(src.steps - 2);
+    if (src.steps == 0) src = enter(src);
     if constexpr (GATHER) {
-      if ((l_steps -= 2) == 0) enter_list();
+      list.steps = uniform(list.steps - 2);
+      if (list.steps == 0) list = enter_list(list);
     }
   };
+  // Codes are decoded among the first half's products and written behind the
+  // barrier; two chunks a thread of the longer conversions would not fit the
+  // registers until then and are decoded as they are written.
+  constexpr bool LATE = NX == 2 && DT == kF16;
   struct Decoded {
     u32x4 a[NX], b[NX];
   };
@@ -585,15 +606,16 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_wide_kernel(WgradArgs args)
   };
 
   Piece now;
-  if (!piece_at<BN, BD>(args, walk, 0, now)) return;
+  if (!piece_at<BN, BD>(walk, 0, now)) return;
   int piece = 0, remaining = now.steps;
   if constexpr (GATHER) {
-    enter_list();
+    list = enter_list(list);
     find(row[0]);
     find(row[1]);
-    if ((l_steps -= 2) == 0) enter_list();
+    list.steps -= 2;
+    if (list.steps == 0) list = enter_list(list);
   }
-  enter();
+  src = enter(src);
   // fill: steps 0 .. 3 in the steady order (dma, codes), steps 0 and 1 decoded
   auto fill = [&](auto sc) {
     constexpr int i = decltype(sc)::value;
@@ -640,7 +662,7 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_wide_kernel(WgradArgs args)
     for (int k = 0; k < 4; ++k) fh[k] = frag_long(sc, 4 + k);
 #pragma unroll
     for (int k = 0; k < 4; ++k) column(0, fl, k);
-    decode(s, d);
+    if constexpr (!LATE) decode(s, d);
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(MUON_WGRAD_VMCNT(BEHIND));
     __builtin_amdgcn_s_waitcnt(0xC07F);       // lgkmcnt(0): stage i + 1's codes are written, stage i is in registers
@@ -648,8 +670,22 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_wide_kernel(WgradArgs args)
     __builtin_amdgcn_sched_barrier(0);
     uint64_t v = 0;
     if constexpr (GATHER) v = check(r);
-    stage(sc, d);
-    dma(sc, v);
+    if constexpr (LATE) {
+      dma(sc, v);
+#pragma unroll
+      for (int x = 0; x < NX; ++x) {
+        __builtin_amdgcn_sched_barrier(0);
+        u32x4 a, b;
+        decode16<DT, FMT>(s.w[x], s.b[x], a, b);
+        const int rr = x_row + 4 * x, o = rr * XROW + ((x_chunk ^ key(rr)) * 32);
+        *(u32x4 *)(xbuf(sc) + o) = a;
+        *(u32x4 *)(xbuf(sc) + (o + 16)) = b;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+      stage(sc, d);
+      dma(sc, v);
+    }
     fetch(s, r);
     if constexpr (GATHER) find(r);
 #pragma unroll
@@ -666,9 +702,10 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_wide_kernel(WgradArgs args)
 
   // the piece is done: to the matrix or to its partial; false: it was the last
   constexpr bool ROWS_LONG = TRANS == LONG_Y;                // the MFMA's rows index the long operand
-  const int rows = TRANS ? args.cols : args.outs, width = TRANS ? args.outs : args.cols;
-  const bool wide_store = !args.accumulate && (((uintptr_t)args.out) & 15) == 0 && (width & 7) == 0;
   auto finish = [&]() -> bool {
+    FarArgs &args = far_args();
+    const int rows = TRANS ? args.cols : args.outs, width = TRANS ? args.outs : args.cols;
+    const bool wide_store = !args.accumulate && (((uintptr_t)args.out) & 15) == 0 && (width & 7) == 0;
     if (now.slot >= 0) {
       float *dst = args.part + ((int64_t)now.slot * 32 * kThreads + tid) * 4;
 #pragma unroll
@@ -720,7 +757,7 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_wide_kernel(WgradArgs args)
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[i][k] = f32x4{};
-    if (!piece_at<BN, BD>(args, walk, ++piece, now)) return false;
+    if (!piece_at<BN, BD>(walk, ++piece, now)) return false;
     remaining = now.steps;
     return true;
   };
@@ -787,12 +824,20 @@ template <int DT, int FMT>
 hipError_t launch_wide(const WgradArgs &args, hipStream_t s) {
   const dim3 g((unsigned)args.blocks), b(kThreads);
 #define MUON_WIDE(TRANS, GATHER)                                                                                             \
-  if (args.wide == 1) hipLaunchKernelGGL((wgrad_wide_kernel<DT, FMT, TRANS, GATHER, 256, 128>), g, b, 0, s, args);           \
-  else hipLaunchKernelGGL((wgrad_wide_kernel<DT, FMT, TRANS, GATHER, 128, 256>), g, b, 0, s, args)
-  if (args.transposed && args.rows_of) MUON_WIDE(true, true);
-  else if (args.transposed) MUON_WIDE(true, false);
-  else if (args.rows_of) MUON_WIDE(false, true);
-  else MUON_WIDE(false, false);
+  if constexpr (FMT == MUON_E4M3) {                                                                                          \
+    if (args.wide == 2) {                                                                                                    \
+      hipLaunchKernelGGL((wgrad_wide_kernel<DT, FMT, TRANS, GATHER, 128, 256>), g, b, 0, s, args);                           \
+      break;                                                                                                                 \
+    }                                                                                                                        \
+  }                                                                                                                          \
+  hipLaunchKernelGGL((wgrad_wide_kernel<DT, FMT, TRANS, GATHER, 256, 128>), g, b, 0, s, args);                               \
+  break
+  switch ((args.transposed ? 2 : 0) + (args.rows_of ? 1 : 0)) {
+    case 0: MUON_WIDE(false, false);
+    case 1: MUON_WIDE(false, true);
+    case 2: MUON_WIDE(true, false);
+    default: MUON_WIDE(true, true);
+  }
 #undef MUON_WIDE
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || args.splits <= 1) return e;
