@@ -7,6 +7,7 @@
 namespace muon {
 
 typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));   // 16 bytes at any 2-byte address
+typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(2)));
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef float f32x2v __attribute__((ext_vector_type(2)));
 
@@ -47,6 +48,29 @@ __device__ __forceinline__ void load8(const typename Val<DT>::type *p, int n, fl
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < n ? Val<DT>::to(p[i]) : 0.0f;
+  }
+}
+
+// p[0 .. n) (n <= 4 used) as fp32, -infinity behind
+template <int DT>
+__device__ __forceinline__ void load4(const typename Val<DT>::type *p, int n, float (&v)[4]) {
+  typedef typename Val<DT>::type T;
+  if (n >= 4) {
+    if constexpr (DT == kF32) {
+      const f32x4u a = *(const f32x4u *)p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = a[i];
+    } else {
+      const u32x2u a = *(const u32x2u *)p;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        v[2 * i] = Val<DT>::to(__builtin_bit_cast(T, (uint16_t)(a[i] & 0xFFFFu)));
+        v[2 * i + 1] = Val<DT>::to(__builtin_bit_cast(T, (uint16_t)(a[i] >> 16)));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < n ? Val<DT>::to(p[i]) : -INFINITY;
   }
 }
 

@@ -1,12 +1,20 @@
 // Routing of tokens to experts: choice, weights and dispatch lists, the
 // gradient of the weights, and the bias step that balances the experts.
 //
-// Forward: a wave takes a token; its lanes hold the token's scores.  Choices
-// are decided in 64 bits, so near-equal ones fall as the definition says.
+// Forward: a wave takes a token, expert lane + 64 r in register r of a lane.
+// Choices are what 64-bit arithmetic says, found in 32 bits wherever those
+// decide: logits order the experts exactly; of score + bias, a pick counts
+// only where its lead over the next choice passes twice the 32-bit error, and
+// a token with a closer pair (about one in 500 of 256 sigmoid scores) is done
+// again in 64 bits.  A pick is a maximum over registers, six cross-lane moves
+// and a ballot, with no LDS.  Weights need the taken logits alone and are
+// computed for all of them at once.
+//
 // The lists are a counting sort by expert that keeps the slots' order: each
 // block counts its own slots, one block an expert turns the counts into the
 // number of slots before, and every slot is then written to its place.
-// Integer counts make every list reproducible.
+// Integer counts make every list reproducible.  A batch of one block does all
+// of it in one launch.
 #include "ckpt_code.h"
 
 namespace muon {
@@ -15,159 +23,322 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
 
-__device__ __forceinline__ double wave_max(double v) {
-  for (int o = 32; o > 0; o >>= 1) v = fmax(v, __shfl_xor(v, o, 64));
-  return v;
-}
-__device__ __forceinline__ double wave_sum(double v) {
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-// the larger value, the lower index among equals; values are never NaN here
-__device__ __forceinline__ void wave_best(double &v, int &at) {
-  for (int o = 32; o > 0; o >>= 1) {
-    const double w = __shfl_xor(v, o, 64);
-    const int i = __shfl_xor(at, o, 64);
-    if (w > v || (w == v && i < at)) v = w, at = i;
-  }
-}
-
 // LDS written by this wave's other lanes is visible
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
 }
 
-constexpr double kNone = -__builtin_huge_val();
-
-// Scores of a token: s[r] of expert lane + 64 r
-template <int R>
-__device__ __forceinline__ void scores(const double (&l)[R], bool sigmoid, double (&s)[R]) {
-  if (sigmoid) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) s[r] = 1.0 / (1.0 + exp(-l[r]));
-    return;
-  }
-  double top = kNone;
-  bool nan = false;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    top = fmax(top, l[r]);
-    nan |= l[r] != l[r];
-  }
-  top = wave_max(top);
-  const bool bad = __any(nan);
-  double z = 0.0;
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    s[r] = l[r] == kNone ? 0.0 : exp(l[r] - top);
-    z += s[r];
-  }
-  z = wave_sum(z);
-#pragma unroll
-  for (int r = 0; r < R; ++r) s[r] = bad ? __builtin_nan("") : (z == 0.0 ? 0.0 : s[r] / z);
+// Reductions over the wave by cross-lane moves (rows of 16, then across rows);
+// lanes without a source see 0.  The result is wave-uniform.
+template <int CTRL>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, moved<0x111>(v));
+  v = max(v, moved<0x112>(v));
+  v = max(v, moved<0x114>(v));
+  v = max(v, moved<0x118>(v));
+  v = max(v, moved<0x142>(v));
+  v = max(v, moved<0x143>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += __uint_as_float(moved<0x111>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x112>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x114>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x118>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x142>(__float_as_uint(v)));
+  v += __uint_as_float(moved<0x143>(__float_as_uint(v)));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
-template <int DT, int R>
-__global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs args) {
-  typedef typename Val<DT>::type T;
-  extern __shared__ __attribute__((aligned(16))) char smem[];
-  const int E = args.experts, K = args.top_k;
-  int *hist = (int *)smem;                                       // [E]
-  int *slot = hist + E;                                          // [kRouteRows * K] ids
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  double *choice = (double *)(smem + (((E + kRouteRows * K) * 4 + 15) & ~15)) + wave * E;   // grouped choice only
-  const int64_t t0 = (int64_t)blockIdx.x * kRouteRows;
-  const int rows = (int)min(args.tokens - t0, (int64_t)kRouteRows);
-  for (int i = threadIdx.x; i < E; i += kThreads) hist[i] = 0;
+// Numbers as unsigned keys of the same order (never 0; -0 counts as 0)
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return u ^ (uint32_t)((int32_t)u >> 31 | (int32_t)0x80000000);
+}
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
+__device__ __forceinline__ uint64_t key_of(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
+  return u ^ (uint64_t)((int64_t)u >> 63 | (int64_t)0x8000000000000000ull);
+}
 
-  for (int q = wave; q < rows; q += kWaves) {
-    const int64_t t = t0 + q;
-    int id = -1;
-    float w = 0.0f;
-    if (!args.token_mask || args.token_mask[t]) {
-      double l[R], s[R], by[R];
-      const T *src = (const T *)args.logits + t * args.ld;
+// The largest key (0: none is left) and the lowest index that has it.
+template <int R>
+__device__ __forceinline__ uint32_t best_of(const uint32_t (&k)[R], int &id) {
+  uint32_t m = k[0];
 #pragma unroll
-      for (int r = 0; r < R; ++r) l[r] = lane + 64 * r < E ? (double)Val<DT>::to(src[lane + 64 * r]) : kNone;
-      scores<R>(l, args.sigmoid, s);
-      bool nan = false;
+  for (int r = 1; r < R; ++r) m = max(m, k[r]);
+  m = wave_max(m);
+  id = -1;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int i = lane + 64 * r;
-        nan |= i < E && s[r] != s[r];
-        double c = s[r] + (args.bias && i < E ? (double)args.bias[i] : 0.0);
-        if (l[r] == kNone || c != c) c = kNone;
-        by[r] = args.bias ? c : l[r];
-        if (args.top_groups < args.groups && i < E) choice[i] = c;
-      }
-      if (__any(nan)) {
-        w = __builtin_nanf("");
-      } else {
-        if (args.top_groups < args.groups) {
-          // lane g holds group g's score; the best top_groups stay
-          const int size = E / args.groups;
-          double best = kNone;
-          int at = lane;
-          wave_sync();
-          if (lane < args.groups) {
-            double a = kNone, b = kNone;
-            for (int i = 0; i < size; ++i) {
-              const double c = choice[lane * size + i];
-              if (c > a) b = a, a = c;
-              else if (c > b) b = c;
-            }
-            best = (args.group_top == 2 && size > 1) ? a + b : a;
-            if (best != best) best = kNone;      // inf - inf
-          }
-          uint64_t kept = 0;
-          bool open = lane < args.groups;
-          for (int n = 0; n < args.top_groups; ++n) {
-            double v = best;
-            int g = open ? at : 1 << 20;
-            if (!open) v = kNone;
-            wave_best(v, g);
-            kept |= 1ull << g;
-            if (g == lane) open = false;
-          }
+  for (int r = R - 1; r >= 0; --r) {
+    const uint64_t b = __ballot(k[r] == m);
+    if (b) id = 64 * r + __ffsll((unsigned long long)b) - 1;
+  }
+  return m;
+}
+template <int R>
+__device__ __forceinline__ uint64_t best_of(const uint64_t (&k)[R], int &id) {
+  uint32_t h = 0;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const int i = lane + 64 * r;
-            if (i < E && !((kept >> (i / size)) & 1)) by[r] = kNone;
-          }
-        }
-        double total = 0.0, mine = 0.0;
-        for (int n = 0; n < K; ++n) {
-          double v = kNone;
-          int i = 1 << 20;
+  for (int r = 0; r < R; ++r) h = max(h, (uint32_t)(k[r] >> 32));
+  h = wave_max(h);
+  uint32_t l = 0;
 #pragma unroll
-          for (int r = 0; r < R; ++r)
-            if (by[r] > v) v = by[r], i = lane + 64 * r;
-          wave_best(v, i);
-          if (v == kNone) break;
-          double p = 0.0;
+  for (int r = 0; r < R; ++r)
+    if ((uint32_t)(k[r] >> 32) == h) l = max(l, (uint32_t)k[r]);
+  l = wave_max(l);
+  const uint64_t m = (uint64_t)h << 32 | l;
+  id = -1;
 #pragma unroll
-          for (int r = 0; r < R; ++r)
-            if (i == lane + 64 * r) p = s[r], by[r] = kNone;
-          p = __shfl(p, i & 63, 64);
-          total += p;
-          if (lane == n) id = i, mine = p;
-        }
-        if (id >= 0) w = (float)(args.scale * (args.renormalize ? (total > 0.0 ? mine / total : 0.0) : mine));
-      }
+  for (int r = R - 1; r >= 0; --r) {
+    const uint64_t b = __ballot(k[r] == m);
+    if (b) id = 64 * r + __ffsll((unsigned long long)b) - 1;
+  }
+  return m;
+}
+template <int R, typename K>
+__device__ __forceinline__ void take_out(K (&k)[R], int id, int lane) {
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (id == lane + 64 * r) k[r] = 0;
+}
+
+// exp(x) within (1 + |x|) 2^-23 of itself
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+// Twice the error of a 32-bit choice.  A sigmoid's exponential is off by (1 +
+// |x|) 2^-23 of itself at most, which moves the score by under 2^-23 (x e^-x /
+// (1 + e^-x) stays under 0.28), the reciprocal by 2^-23, the sum by 2^-24:
+// 2^-21 in all.  A softmax is off by 2^-20 of the largest score: x e^x again,
+// and under 16 roundings of the sum.  The bias adds one rounding.
+__device__ __forceinline__ float lead_wanted(const RouteArgs &args, float largest, float bias_top) {
+  return 2.0f * ((args.sigmoid ? 0x1p-21f : 0x1p-20f) * largest + 0x1p-22f * (largest + bias_top));
+}
+
+// Reductions over the wave (N = 64) or a row of 16 lanes
+template <int N> __device__ __forceinline__ uint32_t max_over(uint32_t v);
+template <int N> __device__ __forceinline__ float sum_over(float v);
+
+// Weight of a taken logit x (have: the lane holds one).  Renormalised ones are
+// formed relative to the largest taken score, which a far logit would
+// otherwise lose (scores that 64 bits hold as 0 stay 0).
+template <int N>
+__device__ __forceinline__ float weight_of(const RouteArgs &args, bool have, float x, float top, float z) {
+  if (args.renormalize) {
+    const uint32_t m = max_over<N>(have ? key_of(x) : 0u);
+    const float far = m ? value_of(m) : 0.0f;
+    float e = 0.0f;
+    if (args.sigmoid) {
+      if (have && far > -709.0f) e = x > 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x - fminf(far, 0.0f)) / (1.0f + expf(x));
+    } else if (have && far - top > -745.0f) {
+      e = expf(x - far);
     }
-    if (lane < K) {
-      args.ids[t * K + lane] = id;
-      args.weights[t * K + lane] = w;
-      slot[q * K + lane] = id;
+    const float total = sum_over<N>(e);
+    return total > 0.0f ? args.scale * (e / total) : 0.0f;
+  }
+  if (!have) return 0.0f;
+  return args.scale * (args.sigmoid ? 1.0f / (1.0f + expf(-x)) : expf(x - top) / z);
+}
+
+template <> __device__ __forceinline__ uint32_t max_over<64>(uint32_t v) { return wave_max(v); }
+template <> __device__ __forceinline__ float sum_over<64>(float v) { return wave_sum(v); }
+
+// Groups that stay, as a bit at g * p for group g; p lanes share a group's
+// scan of its choices in LDS.  lead: by how much the last that stays is ahead.
+template <typename F>
+__device__ __forceinline__ uint64_t groups_that_stay(const RouteArgs &args, const F *choice, int p, int lane, F &lead) {
+  const F none = -(F)INFINITY;
+  const int size = args.experts / args.groups, g = lane / p, sub = lane % p;
+  F a = none, b = none;
+  if (g < args.groups)
+    for (int i = sub; i < size; i += p) {
+      const F c = choice[g * size + i];
+      if (c > a) b = a, a = c;
+      else if (c > b) b = c;
+    }
+  for (int o = 1; o < p; o <<= 1) {
+    const F c = __shfl_xor(a, o, 64), d = __shfl_xor(b, o, 64);
+    b = fmax(fmin(a, c), fmax(b, d));
+    a = fmax(a, c);
+  }
+  F score = (args.group_top == 2 && size > 1) ? a + b : a;
+  if (score != score) score = none;             // inf - inf
+  int rank = 0;
+  for (int i = 0; i < args.groups; ++i) {
+    const F other = __shfl(score, i * p, 64);
+    rank += other > score || (other == score && i < g) ? 1 : 0;
+  }
+  const bool first = g < args.groups && sub == 0;
+  const F in = __shfl(score, __ffsll((unsigned long long)__ballot(first && rank == args.top_groups - 1)) - 1, 64);
+  const F out = __shfl(score, __ffsll((unsigned long long)__ballot(first && rank == args.top_groups)) - 1, 64);
+  lead = in - out;
+  return __ballot(first && rank < args.top_groups);
+}
+
+// What all tokens of a launch share, for a wave a token: the bias, and where
+// an expert's group stands.
+template <int R>
+struct Shared {
+  float bias[R], bias_top;
+  int shift[R], p;
+};
+template <int R>
+__device__ __forceinline__ void load_shared(const RouteArgs &args, int lane, Shared<R> &s) {
+  const int E = args.experts;
+  s.bias_top = 0.0f;
+  s.p = 1;
+  if (args.top_groups < args.groups)
+    while (2 * s.p * args.groups <= 64) s.p *= 2;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = lane + 64 * r;
+    s.bias[r] = args.bias && i < E ? args.bias[i] : 0.0f;
+    s.bias_top = fmaxf(s.bias_top, fabsf(s.bias[r]));
+    s.shift[r] = args.top_groups < args.groups && i < E ? i / (E / args.groups) * s.p : 0;
+  }
+  s.bias_top = __uint_as_float(wave_max(__float_as_uint(s.bias_top)));
+}
+
+// One token by one wave: lane j of the first top_k gets the j-th id (-1: none)
+// and weight.  exact: in 64 bits at once.
+template <int DT, int R>
+__device__ __forceinline__ void route_token(const RouteArgs &args, int64_t t, const Shared<R> &sh, bool exact, void *scratch, int lane,
+                                            int &id, float &w) {
+  typedef typename Val<DT>::type T;
+  const int E = args.experts, K = args.top_k;
+  const bool grouped = args.top_groups < args.groups, biased = args.bias != nullptr;
+  const T *src = (const T *)args.logits + t * args.ld;
+  id = -1;
+  w = 0.0f;
+  float l[R];
+  bool nan = false;
+  uint32_t mk = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    l[r] = lane + 64 * r < E ? Val<DT>::to(src[lane + 64 * r]) : -INFINITY;
+    nan |= l[r] != l[r];
+    mk = max(mk, l[r] == -INFINITY ? 0u : key_of(l[r]));
+  }
+  bool bad = __any(nan);
+  float top = 0.0f, z = 1.0f;
+  if (!args.sigmoid) {
+    mk = wave_max(mk);
+    top = mk ? value_of(mk) : 0.0f;
+    bad |= top == INFINITY;                 // inf - inf
+    if (biased || grouped || !args.renormalize) {
+      z = 0.0f;
+#pragma unroll
+      for (int r = 0; r < R; ++r) z += expf(l[r] - top);
+      z = wave_sum(z);
     }
   }
-  if (!args.lists) return;
+  if (bad) {
+    w = __builtin_nanf("");
+    return;
+  }
+  bool close = exact;
+  if (!close) {
+    uint32_t k[R];
+    float c[R], wanted = 0.0f;
+    if (grouped || biased) {
+      const float largest = args.sigmoid ? 1.0f : 1.0f / z;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float s = args.sigmoid ? __builtin_amdgcn_rcpf(1.0f + expf(-l[r])) : expf(l[r] - top) * largest;
+        c[r] = s + sh.bias[r];
+        if (l[r] == -INFINITY || c[r] != c[r]) c[r] = -INFINITY;
+      }
+      wanted = lead_wanted(args, largest, sh.bias_top);
+    }
+    uint64_t stay = ~0ull;
+    if (grouped) {
+      float *choice = (float *)scratch, lead;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (lane + 64 * r < E) choice[lane + 64 * r] = c[r];
+      wave_sync();
+      stay = groups_that_stay<float>(args, choice, sh.p, lane, lead);
+      wave_sync();
+      close = !(lead > 2.0f * wanted);       // a score is a sum of two choices
+    }
+    if (!close) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float v = biased ? c[r] : l[r];
+        k[r] = v == -INFINITY || !((stay >> sh.shift[r]) & 1) ? 0u : key_of(v);
+      }
+      uint32_t before = 0;
+      for (int n = 0; n < K + (biased ? 1 : 0); ++n) {
+        int e;
+        const uint32_t m = best_of<R>(k, e);
+        if (m == 0) break;
+        if (biased && n > 0 && !(value_of(before) - value_of(m) > wanted)) {
+          close = true;
+          break;
+        }
+        if (lane == n && n < K) id = e;
+        take_out<R>(k, e, lane);
+        before = m;
+      }
+    }
+  }
+  if (close) {
+    double d[R];
+    double zz = 0.0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      d[r] = args.sigmoid ? 1.0 / (1.0 + exp(-(double)l[r])) : exp((double)l[r] - (double)top);
+      if (lane + 64 * r < E) zz += d[r];
+    }
+    if (!args.sigmoid)
+      for (int o = 32; o > 0; o >>= 1) zz += __shfl_xor(zz, o, 64);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      d[r] = (args.sigmoid ? d[r] : d[r] / zz) + (double)sh.bias[r];
+      if (l[r] == -INFINITY || d[r] != d[r]) d[r] = -INFINITY;
+    }
+    uint64_t stay = ~0ull;
+    if (grouped) {
+      double *choice = (double *)scratch, lead;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (lane + 64 * r < E) choice[lane + 64 * r] = d[r];
+      wave_sync();
+      stay = groups_that_stay<double>(args, choice, sh.p, lane, lead);
+      wave_sync();
+    }
+    id = -1;
+    uint64_t k[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const double v = biased ? d[r] : (double)l[r];
+      k[r] = v == -INFINITY || !((stay >> sh.shift[r]) & 1) ? 0ull : key_of(v);
+    }
+    for (int n = 0; n < K; ++n) {
+      int e;
+      if (best_of<R>(k, e) == 0) break;
+      if (lane == n) id = e;
+      take_out<R>(k, e, lane);
+    }
+  }
+  w = weight_of<64>(args, id >= 0, id >= 0 ? Val<DT>::to(src[id]) : -INFINITY, top, z);
+}
+
+// A block's share of the lists, from its tokens' ids in slot: its slots of each
+// expert and each slot's place among them, or, of a block alone, the lists.
+__device__ __forceinline__ void make_lists(const RouteArgs &args, int *hist, int *slot, int rows, int64_t t0) {
+  const int E = args.experts, K = args.top_k, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int i = threadIdx.x; i < E; i += blockDim.x) hist[i] = 0;
   __syncthreads();
   // place of each slot among the block's slots of its expert, 64 slots at a
   // time: the lanes with an equal id are found from one ballot a bit
+  const int n = rows * K;
+  int *place = args.blocks == 1 ? slot + args.rows_per_block * K : nullptr;     // a block alone keeps them in LDS
   if (wave == 0) {
-    const int n = rows * K;
     int bits = 0;
     while ((1 << bits) < E) ++bits;
     for (int base = 0; base < n; base += 64) {
@@ -181,7 +352,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs args) {
       if (id >= 0) {
         const int before = __popcll(same & ((1ull << lane) - 1));
         const int had = hist[id];
-        args.rank[t0 * K + i] = had + before;
+        if (place) place[i] = had + before;
+        else args.rank[t0 * K + i] = had + before;
         wave_sync();
         if (same >> lane == 1) hist[id] = had + before + 1;    // the last of them
       }
@@ -189,7 +361,320 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs args) {
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < E; i += kThreads) args.hist[(int64_t)i * args.blocks + blockIdx.x] = hist[i];
+  if (!place) {
+    for (int i = threadIdx.x; i < E; i += blockDim.x) args.hist[(int64_t)i * args.blocks + blockIdx.x] = hist[i];
+    return;
+  }
+  if (wave == 0) {
+    int before = 0;
+    for (int base = 0; base < E; base += 64) {
+      const int i = base + lane;
+      const int v = i < E ? hist[i] : 0;
+      int sum = v;
+      for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(sum, o, 64);
+        if (lane >= o) sum += u;
+      }
+      if (i < E) {
+        args.counts[i] = v;
+        if (args.load) args.load[i] += v;
+        hist[i] = before + sum - v;
+      }
+      before += __shfl(sum, 63, 64);
+    }
+    if (lane == 0) hist[E] = before;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i <= E; i += blockDim.x) args.offsets[i] = hist[i];
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int id = slot[i];
+    if (id >= 0) {
+      args.order[hist[id] + place[i]] = i;
+      args.rows[hist[id] + place[i]] = i / K;
+    }
+    if (i >= hist[E]) args.order[i] = args.rows[i] = -1;
+  }
+}
+
+// More experts, picks or groups than the kernel below takes: a wave a token.
+template <int DT, int R>
+__global__ __launch_bounds__(R <= 8 ? 512 : 256) void route_kernel(RouteArgs args) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int E = args.experts, K = args.top_k;
+  const int waves = blockDim.x >> 6, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int *hist = (int *)smem;                                       // [E + 1]
+  int *slot = hist + E + 1;                                      // [rows_per_block * K] ids, then places
+  char *scratch = smem + (((size_t)(E + 1 + args.rows_per_block * K) * 4 + 15) & ~(size_t)15) + (size_t)wave * E * 8;   // grouped only
+  const int64_t t0 = (int64_t)blockIdx.x * args.rows_per_block;
+  const int rows = (int)min(args.tokens - t0, (int64_t)args.rows_per_block);
+  Shared<R> sh;
+  load_shared<R>(args, lane, sh);
+  for (int q = wave; q < rows; q += waves) {
+    const int64_t t = t0 + q;
+    int id = -1;
+    float w = 0.0f;
+    if (!args.token_mask || args.token_mask[t]) route_token<DT, R>(args, t, sh, false, scratch, lane, id, w);
+    if (lane < K) {
+      args.ids[t * K + lane] = id;
+      args.weights[t * K + lane] = w;
+      if (args.lists) slot[q * K + lane] = id;
+    }
+  }
+  if (args.lists) make_lists(args, hist, slot, rows, t0);
+}
+
+// ---------------------------------------------------------------------------
+// Up to 256 experts, 16 taken, 16 groups: a wave takes four tokens, 16 lanes
+// (one DPP row) each.  Lane l of a row holds experts 64 c + 4 l + q in register
+// v = 4 c + q; within a lane and across lanes of a register, indices ascend.
+// Everything of a token is uniform over its row.
+
+// Reductions over a row of 16 lanes by rotations, in every lane
+template <int CTRL>
+__device__ __forceinline__ uint32_t turned(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = max(v, turned<0x128>(v));
+  v = max(v, turned<0x124>(v));
+  v = max(v, turned<0x122>(v));
+  return max(v, turned<0x121>(v));
+}
+__device__ __forceinline__ uint32_t row_min(uint32_t v) {
+  v = min(v, turned<0x128>(v));
+  v = min(v, turned<0x124>(v));
+  v = min(v, turned<0x122>(v));
+  return min(v, turned<0x121>(v));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += __uint_as_float(turned<0x128>(__float_as_uint(v)));
+  v += __uint_as_float(turned<0x124>(__float_as_uint(v)));
+  v += __uint_as_float(turned<0x122>(__float_as_uint(v)));
+  return v + __uint_as_float(turned<0x121>(__float_as_uint(v)));
+}
+
+template <> __device__ __forceinline__ uint32_t max_over<16>(uint32_t v) { return row_max(v); }
+template <> __device__ __forceinline__ float sum_over<16>(float v) { return row_sum(v); }
+
+constexpr uint32_t kNobody = 0xFFFFu;
+constexpr int kRedo = -2;
+
+// The row's largest key (0: none is left) and the lowest expert that has it,
+// which is taken out.
+template <int V>
+__device__ __forceinline__ uint32_t take_best(uint32_t (&k)[V], int l16, uint32_t &id) {
+  uint32_t m = k[0];
+#pragma unroll
+  for (int v = 1; v < V; ++v) m = max(m, k[v]);
+  m = row_max(m);
+  int at = -1;
+#pragma unroll
+  for (int v = V - 1; v >= 0; --v) at = k[v] == m ? v : at;
+  const uint32_t e = at < 0 ? kNobody : (uint32_t)((at >> 2) * 64 + l16 * 4 + (at & 3));
+  id = row_min(e);
+  at = e == id ? at : -1;
+#pragma unroll
+  for (int v = 0; v < V; ++v) k[v] = at == v ? 0u : k[v];
+  return m;
+}
+// The groups that stay, as a bit at g * p for group g (p lanes share a group),
+// and by how much the last of them is ahead of the first that goes.
+template <typename F, int V>
+__device__ __forceinline__ uint32_t row_groups(const RouteArgs &args, const F (&c)[V], F *choice, int p, int lane, F &lead) {
+  const F none = -(F)INFINITY;
+  const int E = args.experts, l16 = lane & 15, size = E / args.groups, g = l16 / p, sub = l16 % p;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = (v >> 2) * 64 + l16 * 4 + (v & 3);
+    if (e < E) choice[e] = c[v];
+  }
+  wave_sync();
+  F a = none, b = none;
+  const int n = (size - sub + p - 1) / p;       // this lane's choices, from a place of its own: distinct banks
+  if (g < args.groups && n > 0) {
+    int at = l16 % n;
+    for (int i = 0; i < n; ++i) {
+      const F x = choice[g * size + sub + at * p];
+      b = fmax(b, fmin(a, x));
+      a = fmax(a, x);
+      at = at + 1 == n ? 0 : at + 1;
+    }
+  }
+  wave_sync();
+  for (int o = 1; o < p; o <<= 1) {
+    const F x = __shfl_xor(a, o, 64), y = __shfl_xor(b, o, 64);
+    b = fmax(fmin(a, x), fmax(b, y));
+    a = fmax(a, x);
+  }
+  F score = (args.group_top == 2 && size > 1) ? a + b : a;
+  if (score != score) score = none;             // inf - inf
+  int rank = 0;
+  for (int i = 0; i < args.groups; ++i) {
+    const F other = __shfl(score, (lane & 48) + i * p, 64);
+    rank += other > score || (other == score && i < g) ? 1 : 0;
+  }
+  const bool mine = g < args.groups && sub == 0, in = mine && rank < args.top_groups;
+  F least = in ? score : (F)INFINITY, most = mine && !in ? score : none;
+  for (int o = 8; o > 0; o >>= 1) {
+    least = fmin(least, __shfl_xor(least, o, 64));
+    most = fmax(most, __shfl_xor(most, o, 64));
+  }
+  lead = least - most;
+  return (uint32_t)(__ballot(in) >> (lane & 48)) & 0xFFFFu;
+}
+
+template <int DT, int V>
+__global__ __launch_bounds__(512) void route_rows_kernel(RouteArgs args) {
+  typedef typename Val<DT>::type T;
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int E = args.experts, K = args.top_k;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, wave = threadIdx.x >> 6;
+  int *hist = (int *)smem;                                       // [E + 1]
+  int *slot = hist + E + 1;                                      // [rows_per_block * K] ids, then places
+  const bool grouped = args.top_groups < args.groups, biased = args.bias != nullptr;
+  char *scratch = smem + (((size_t)(E + 1 + args.rows_per_block * K) * 4 + 15) & ~(size_t)15);   // grouped only
+  const int64_t t0 = (int64_t)blockIdx.x * args.rows_per_block;
+  const int rows = (int)min(args.tokens - t0, (int64_t)args.rows_per_block);
+
+  // where an expert's group stands, 4 bits a register; the bias's largest
+  int p = 1;
+  uint32_t shift[(V + 7) / 8] = {};
+  float bias[V], bias_top = 0.0f;
+  if (grouped) {
+    while (2 * p * args.groups <= 16) p *= 2;
+    const int size = E / args.groups;
+#pragma unroll
+    for (int v = 0; v < V; ++v) shift[v / 8] |= (uint32_t)(min((v >> 2) * 64 + l16 * 4 + (v & 3), E - 1) / size * p) << (4 * (v & 7));
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = (v >> 2) * 64 + l16 * 4 + (v & 3);
+    bias[v] = biased && e < E ? args.bias[e] : 0.0f;
+    bias_top = fmaxf(bias_top, fabsf(bias[v]));
+  }
+  if (biased) bias_top = __uint_as_float(row_max(__float_as_uint(bias_top)));
+
+  for (int q = wave * 4; q < rows; q += blockDim.x / 16) {       // wave-uniform
+    const int mine = q + (lane >> 4);
+    const bool live = mine < rows && (!args.token_mask || args.token_mask[t0 + mine]);
+    const int64_t t = t0 + min(mine, rows - 1);
+    const T *src = (const T *)args.logits + t * args.ld;
+    float l[V];
+    bool nan = false;
+    uint32_t mk = 0;
+#pragma unroll
+    for (int c = 0; c < V / 4; ++c) {
+      float x[4];
+      load4<DT>(src + c * 64 + l16 * 4, E - c * 64 - l16 * 4, x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[4 * c + i] = x[i];
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      nan |= l[v] != l[v];
+      mk = max(mk, l[v] == -INFINITY ? 0u : key_of(l[v]));
+    }
+    bool bad = row_max(nan ? 1u : 0u) != 0;
+    float top = 0.0f, z = 1.0f;
+    if (!args.sigmoid) {
+      mk = row_max(mk);
+      top = mk ? value_of(mk) : 0.0f;
+      bad |= top == INFINITY;                     // inf - inf
+      if (biased || grouped || !args.renormalize) {
+        z = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) z += exp_fast(l[v] - top);
+        z = row_sum(z);
+      }
+    }
+    float c[V], wanted = 0.0f;
+    if (grouped || biased) {
+      const float largest = args.sigmoid ? 1.0f : 1.0f / z;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float s = args.sigmoid ? __builtin_amdgcn_rcpf(1.0f + exp_fast(-l[v])) : exp_fast(l[v] - top) * largest;
+        c[v] = s + bias[v];
+        if (l[v] == -INFINITY || c[v] != c[v]) c[v] = -INFINITY;
+      }
+      wanted = lead_wanted(args, largest, bias_top);
+    }
+    uint32_t stay = 0xFFFFu;
+    bool close = false;
+    if (grouped) {
+      float lead;
+      stay = row_groups<float, V>(args, c, (float *)scratch + (threadIdx.x >> 4) * E, p, lane, lead);
+      close = !(lead > 2.0f * wanted);          // a score is a sum of two choices
+    }
+    uint32_t k[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float x = biased ? c[v] : l[v];
+      k[v] = x == -INFINITY || !((stay >> ((shift[v / 8] >> (4 * (v & 7))) & 15)) & 1) ? 0u : key_of(x);
+    }
+    // Lane n of the row keeps the n-th pick.  With a bias, each pick's lead over
+    // the next has to pass the 32-bit error, or the two are compared in 64
+    // bits (sigmoids; a softmax needs the whole sum for that), and so has the
+    // last pick's over all that come near it.
+    uint32_t id = kNobody, last = kNobody, before = 0;
+    bool open = live && !bad && !close;
+    for (int n = 0; n < E; ++n) {
+      if (!biased && n == K) break;
+      uint32_t e;
+      const uint32_t m = take_best<V>(k, l16, e);
+      if (m == 0) open = false;
+      if (biased && n > 0 && open) {
+        if (value_of(before) - value_of(m) > wanted) {
+          if (n >= K) open = false;
+        } else {
+          const float x = Val<DT>::to(src[last]), y = Val<DT>::to(src[e]);
+          const float bx = args.bias[last], by = args.bias[e];
+          bool ordered = x == y && bx == by && last < e;
+          if (!ordered && args.sigmoid) {
+            const double dx = 1.0 / (1.0 + exp(-(double)x)) + (double)bx, dy = 1.0 / (1.0 + exp(-(double)y)) + (double)by;
+            ordered = dx > dy || (dx == dy && last < e);
+          }
+          if (!ordered) {
+            close = true;
+            open = false;
+          }
+        }
+      }
+      if (open && n < K) {
+        if (l16 == n) id = e;
+        last = e;                                // from the last pick on, all are compared with it
+        before = m;
+      }
+      if (!__any(open)) break;
+    }
+    const bool redo = close && live && !bad, have = id != kNobody && !redo;
+    float w = weight_of<16>(args, have, have ? Val<DT>::to(src[id]) : -INFINITY, top, z);
+    if (bad && live) w = __builtin_nanf("");
+    if (mine < rows && l16 < K) {
+      const int out = redo ? kRedo : have ? (int)id : -1;
+      slot[mine * K + l16] = out;
+      args.ids[t * K + l16] = out;
+      args.weights[t * K + l16] = w;
+    }
+  }
+  // tokens that 32 bits leave open: a wave a token, in 64 bits
+  __syncthreads();
+  constexpr int R = V / 4;
+  Shared<R> sh;
+  bool loaded = false;
+  for (int q = wave; q < rows; q += blockDim.x / 64) {
+    if (slot[q * K] != kRedo) continue;
+    if (!loaded) load_shared<R>(args, lane, sh);
+    loaded = true;
+    int id;
+    float w;
+    route_token<DT, R>(args, t0 + q, sh, true, (double *)scratch + wave * E, lane, id, w);
+    if (lane < K) {
+      slot[q * K + lane] = id;
+      args.ids[(t0 + q) * K + lane] = id;
+      args.weights[(t0 + q) * K + lane] = w;
+    }
+  }
+  if (args.lists) make_lists(args, hist, slot, rows, t0);
 }
 
 // hist[e][.] -> slots of expert e in the blocks before; counts[e]
@@ -246,8 +731,8 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(RouteArgs args) {
   __syncthreads();
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i <= E; i += kThreads) args.offsets[i] = offset[i];
-  const int64_t t0 = (int64_t)blockIdx.x * kRouteRows;
-  const int n = (int)min(args.tokens - t0, (int64_t)kRouteRows) * K;
+  const int64_t t0 = (int64_t)blockIdx.x * args.rows_per_block;
+  const int n = (int)min(args.tokens - t0, (int64_t)args.rows_per_block) * K;
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const int64_t flat = t0 * K + i;
     const int id = args.ids[flat];
@@ -359,13 +844,25 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(float *bias, const C 
 
 template <int DT>
 hipError_t route_for(const RouteArgs &args, hipStream_t s) {
-  const size_t lists = ((size_t)(args.experts + kRouteRows * args.top_k) * 4 + 15) & ~(size_t)15;
-  const size_t lds = lists + (args.top_groups < args.groups ? (size_t)kWaves * args.experts * 8 : 0);
-  const dim3 g(args.blocks), b(kThreads);
+  const bool alone = args.lists && args.blocks == 1, grouped = args.top_groups < args.groups;
+  const size_t lists = ((size_t)(args.experts + 1 + args.rows_per_block * args.top_k) * 4 + 15) & ~(size_t)15;
+  // the groups' choices, and a lone block's places, follow the slots
+  const size_t places = alone ? (size_t)args.rows_per_block * args.top_k * 4 : 0;
+  const dim3 g(args.blocks);
+  if (args.experts <= 256 && args.top_k <= 16 && (!grouped || args.groups <= 16)) {
+    const int waves = (int)min((args.tokens + 3) / 4, (int64_t)8);
+    const size_t lds = lists + max(grouped ? (size_t)waves * 4 * args.experts * 4 : (size_t)0, places);
+    const dim3 b(waves * 64);
+    if (args.experts <= 64) hipLaunchKernelGGL((route_rows_kernel<DT, 4>), g, b, lds, s, args);
+    else if (args.experts <= 128) hipLaunchKernelGGL((route_rows_kernel<DT, 8>), g, b, lds, s, args);
+    else hipLaunchKernelGGL((route_rows_kernel<DT, 16>), g, b, lds, s, args);
+    return hipGetLastError();
+  }
+  const int waves = (int)min(args.tokens, (int64_t)(args.experts > 512 ? 4 : 8));
+  const size_t lds = lists + max(grouped ? (size_t)waves * args.experts * 8 : (size_t)0, places);
+  const dim3 b(waves * 64);
   const int r = (args.experts + 63) / 64;
-  if (r <= 1) hipLaunchKernelGGL((route_kernel<DT, 1>), g, b, lds, s, args);
-  else if (r <= 2) hipLaunchKernelGGL((route_kernel<DT, 2>), g, b, lds, s, args);
-  else if (r <= 4) hipLaunchKernelGGL((route_kernel<DT, 4>), g, b, lds, s, args);
+  if (r <= 4) hipLaunchKernelGGL((route_kernel<DT, 4>), g, b, lds, s, args);
   else if (r <= 8) hipLaunchKernelGGL((route_kernel<DT, 8>), g, b, lds, s, args);
   else hipLaunchKernelGGL((route_kernel<DT, 16>), g, b, lds, s, args);
   return hipGetLastError();
@@ -391,7 +888,7 @@ hipError_t launch_route(const RouteArgs &args, int dtype, hipStream_t s) {
     e = dtype == kF32 ? route_for<kF32>(args, s) : dtype == kBF16 ? route_for<kBF16>(args, s) : route_for<kF16>(args, s);
     if (e != hipSuccess) return e;
   }
-  if (!args.lists) return e;
+  if (!args.lists || args.blocks == 1) return e;
   hipLaunchKernelGGL(route_scan_kernel, dim3(args.experts), dim3(kThreads), 0, s, args);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL(route_place_kernel, dim3(args.blocks > 0 ? args.blocks : 1), dim3(kThreads), (size_t)(args.experts + 1) * 4, s, args);

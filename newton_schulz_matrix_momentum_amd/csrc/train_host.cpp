@@ -245,7 +245,10 @@ muon_status check_groups(const muon_routing *a) {
   return MUON_OK;
 }
 
-int64_t route_blocks(const muon_routing *a) { return (a->tokens + kRouteRows - 1) / kRouteRows; }
+int64_t route_rows(const muon_routing *a) {
+  return a->tokens <= kRouteAlone ? kRouteAlone : kRouteRows;
+}
+int64_t route_blocks(const muon_routing *a) { return (a->tokens + route_rows(a) - 1) / route_rows(a); }
 
 size_t route_bytes(const muon_routing *a) {
   if (!a->counts) return 256;
@@ -270,6 +273,7 @@ RouteArgs route_args(const muon_routing *a) {
   x.sigmoid = a->score == MUON_SIGMOID;
   x.renormalize = a->renormalize != 0;
   x.scale = a->scale;
+  x.rows_per_block = (int32_t)route_rows(a);
   x.blocks = (int32_t)route_blocks(a);
   return x;
 }

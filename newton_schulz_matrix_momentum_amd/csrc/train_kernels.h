@@ -89,7 +89,8 @@ hipError_t launch_wgrad_join(const WgradArgs &args, hipStream_t s);
 constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxTopK = 64;
 constexpr int kRouteMaxGroups = 64;
-constexpr int kRouteRows = 64;             // tokens of a block
+constexpr int kRouteRows = 32;             // tokens of a block
+constexpr int kRouteAlone = 64;            // up to so many tokens one block does everything
 
 struct RouteArgs {
   const void *logits;
@@ -111,7 +112,7 @@ struct RouteArgs {
   int32_t sigmoid, renormalize;
   int32_t lists;           // the dispatch lists are wanted
   float scale;
-  int32_t blocks;
+  int32_t rows_per_block, blocks;
 };
 
 hipError_t launch_route(const RouteArgs &args, int dtype, hipStream_t s);
