@@ -74,6 +74,27 @@ __device__ __forceinline__ void load4(const typename Val<DT>::type *p, int n, fl
   }
 }
 
+// n of v[0 .. 4) to p
+template <int DT>
+__device__ __forceinline__ void store4(typename Val<DT>::type *p, int n, const float *v) {
+  if (n >= 4) {
+    if constexpr (DT == kF32) {
+      *(f32x4u *)p = f32x4u{v[0], v[1], v[2], v[3]};
+    } else {
+      u32x2u a;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        a[i] = (uint32_t)__builtin_bit_cast(uint16_t, Val<DT>::from(v[2 * i])) |
+               ((uint32_t)__builtin_bit_cast(uint16_t, Val<DT>::from(v[2 * i + 1])) << 16);
+      *(u32x2u *)p = a;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = Val<DT>::from(v[i]);
+  }
+}
+
 template <int DT>
 __device__ __forceinline__ void store8(typename Val<DT>::type *p, int n, const float (&v)[8]) {
   if (n >= 8) {

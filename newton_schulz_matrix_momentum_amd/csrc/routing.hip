@@ -17,6 +17,8 @@
 // of it in one launch.
 #include "ckpt_code.h"
 
+#include <type_traits>
+
 namespace muon {
 namespace {
 
@@ -677,28 +679,52 @@ __global__ __launch_bounds__(512) void route_rows_kernel(RouteArgs args) {
   if (args.lists) make_lists(args, hist, slot, rows, t0);
 }
 
-// hist[e][.] -> slots of expert e in the blocks before; counts[e]
+// Inclusive sum over the wave by cross-lane moves
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+}
+
+// Sum over the threads before this one; all: over the block.  part: kWaves ints of LDS
+__device__ __forceinline__ int block_before(int v, int *part, int &all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int sum = wave_scan(v);
+  if (lane == 63) part[wave] = sum;
+  __syncthreads();
+  int before = sum - v;
+  all = 0;
+  for (int w = 0; w < kWaves; ++w) {
+    before += w < wave ? part[w] : 0;
+    all += part[w];
+  }
+  return before;
+}
+
+// hist[e][.] -> slots of expert e in the blocks before; counts[e].  A thread
+// takes a run of up to four blocks at a time.
 __global__ __launch_bounds__(kThreads) void route_scan_kernel(RouteArgs args) {
   __shared__ int part[kWaves];
-  const int e = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = blockIdx.x;
   int *h = args.hist + (int64_t)e * args.blocks;
   int before = 0;
-  for (int base = 0; base < args.blocks; base += kThreads) {
-    const int i = base + (int)threadIdx.x;
-    const int v = i < args.blocks ? h[i] : 0;
-    int sum = v;
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(sum, o, 64);
-      if (lane >= o) sum += u;
+  for (int base = 0; base < args.blocks; base += 4 * kThreads) {
+    const int per = min((args.blocks - base + kThreads - 1) / kThreads, 4), first = base + (int)threadIdx.x * per;
+    int v[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = i < per && first + i < args.blocks ? h[first + i] : 0;
+      sum += v[i];
     }
-    if (lane == 63) part[wave] = sum;
-    __syncthreads();
-    int add = before, all = 0;
-    for (int w = 0; w < kWaves; ++w) {
-      if (w < wave) add += part[w];
-      all += part[w];
+    int all, at = before + block_before(sum, part, all);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < per && first + i < args.blocks) h[first + i] = at;
+      at += v[i];
     }
-    if (i < args.blocks) h[i] = add + sum - v;
     before += all;
     __syncthreads();
   }
@@ -709,45 +735,147 @@ __global__ __launch_bounds__(kThreads) void route_scan_kernel(RouteArgs args) {
 }
 
 // every slot to its place; places past the last slot hold -1
+constexpr int kPlaceSlots = 4 * kThreads;      // of a block
 __global__ __launch_bounds__(kThreads) void route_place_kernel(RouteArgs args) {
-  extern __shared__ __attribute__((aligned(16))) char smem[];
-  int *offset = (int *)smem;     // [E + 1]
-  const int E = args.experts, K = args.top_k;
-  if (threadIdx.x < 64) {
-    int before = 0;
-    for (int base = 0; base < E; base += 64) {
-      const int i = base + (int)threadIdx.x;
-      const int v = i < E ? args.counts[i] : 0;
-      int sum = v;
-      for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(sum, o, 64);
-        if ((int)threadIdx.x >= o) sum += u;
-      }
-      if (i < E) offset[i] = before + sum - v;
-      before += __shfl(sum, 63, 64);
+  static_assert(kRouteMaxExperts <= 4 * kThreads, "four experts a thread");
+  __shared__ int offset[kRouteMaxExperts + 1], part[kWaves];
+  const int E = args.experts, K = args.top_k, tid = threadIdx.x;
+  {
+    int v[4], sum = 0, all;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = 4 * tid + i < E ? args.counts[4 * tid + i] : 0;
+      sum += v[i];
     }
-    if (threadIdx.x == 0) offset[E] = before;
+    int at = block_before(sum, part, all);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (4 * tid + i <= E) offset[4 * tid + i] = at;
+      at += v[i];
+    }
+    if (tid == 0) offset[E] = all;
   }
   __syncthreads();
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= E; i += kThreads) args.offsets[i] = offset[i];
-  const int64_t t0 = (int64_t)blockIdx.x * args.rows_per_block;
-  const int n = (int)min(args.tokens - t0, (int64_t)args.rows_per_block) * K;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int64_t flat = t0 * K + i;
+    for (int i = tid; i <= E; i += kThreads) args.offsets[i] = offset[i];
+  const int64_t total = args.tokens * K;
+  const int slots = args.rows_per_block * K;   // of a block of the first kernel
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t flat = (int64_t)blockIdx.x * kPlaceSlots + i * kThreads + tid;
+    if (flat >= total) break;
     const int id = args.ids[flat];
     if (id >= 0) {
-      const int place = offset[id] + args.hist[(int64_t)id * args.blocks + blockIdx.x] + args.rank[flat];
+      const int place = offset[id] + args.hist[(int64_t)id * args.blocks + (int)flat / slots] + args.rank[flat];
       args.order[place] = (int)flat;
-      args.rows[place] = (int)(flat / K);
+      args.rows[place] = (int)flat / K;
     }
     if (flat >= offset[E]) args.order[flat] = args.rows[flat] = -1;
   }
 }
 
-// One wave a token: lanes hold the scores and their gradients.  With weights
-// renormalised over the taken experts, a softmax's gradient outside them is
-// zero (their weights are a softmax of the taken logits alone).
+// Sums over a row of 16 lanes and broadcasts from its lane J, in every lane
+template <int J>
+__device__ __forceinline__ uint32_t row_lane(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x150 + J, 0xF, 0xF, true);
+}
+
+template <int I, int N, typename F>
+__device__ __forceinline__ void each(F &&f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    each<I + 1, N>(f);
+  }
+}
+
+// Gradient of the weights.  With p_j the taken scores and d_j the gradient of
+// each:  d_j = scale dw_j, or scale (dw_j - sum dw p / Z) / Z renormalised over
+// Z = sum p;  softmax: s (d - sum d p) over all experts;  sigmoid: s (1 - s) d.
+// A softmax's renormalised weights are a softmax of the taken logits alone:
+// no other logit enters, and the sum above is zero.
+template <typename Sum>
+__device__ __forceinline__ float pick_gradient(const RouteArgs &args, bool have, float dw, float p, Sum &&sum) {
+  float d = dw;
+  if (args.renormalize) {
+    const float total = sum(p), dot = sum(dw * p);
+    d = have && total > 0.0f ? (dw - dot / total) / total : 0.0f;
+  }
+  return d * args.scale;
+}
+
+// Up to 256 experts and 16 picks: four tokens a wave, in the layout of the
+// forward kernel; lane j of a row holds pick j.
+template <int DT, int V>
+__global__ __launch_bounds__(kThreads) void route_rows_backward_kernel(RouteArgs args) {
+  typedef typename Val<DT>::type T;
+  const int E = args.experts, K = args.top_k, l16 = threadIdx.x & 15;
+  const int64_t token = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 4;
+  const bool live = token < args.tokens;
+  const int64_t t = live ? token : args.tokens - 1;
+  const T *src = (const T *)args.logits + t * args.ld;
+  int id = l16 < K ? args.ids[t * K + l16] : -1;
+  if (id < 0 || id >= E) id = -1;
+  const bool have = id >= 0;
+  const float dw = have ? args.grad_weights[t * K + l16] : 0.0f;
+  const float x = have ? Val<DT>::to(src[id]) : 0.0f;
+  const bool dense = !args.sigmoid && !args.renormalize;       // every score has a gradient
+  float l[V], top = 0.0f, inv = 1.0f, p;
+  if (dense) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int c = 0; c < V / 4; ++c) {
+      float y[4];
+      load4<DT>(src + c * 64 + l16 * 4, E - c * 64 - l16 * 4, y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        l[4 * c + i] = y[i];
+        m = max(m, y[i] == -INFINITY ? 0u : key_of(y[i]));
+      }
+    }
+    m = row_max(m);
+    top = m ? value_of(m) : 0.0f;
+    float z = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      l[v] = expf(l[v] - top);
+      z += l[v];
+    }
+    inv = 1.0f / row_sum(z);
+    p = have ? expf(x - top) * inv : 0.0f;
+  } else if (args.sigmoid) {
+    p = have ? 1.0f / (1.0f + expf(-x)) : 0.0f;
+  } else {
+    const uint32_t m = row_max(have ? key_of(x) : 0u);
+    p = have ? expf(x - value_of(m)) : 0.0f;                   // relative to the largest taken: only ratios matter
+  }
+  float d = pick_gradient(args, have, dw, p, [](float v) { return row_sum(v); });
+  // what lands on the picked logit itself
+  float mine = !have ? 0.0f : args.sigmoid ? p * (1.0f - p) * d : dense ? d : p * d;
+  const float dot = dense ? row_sum(have ? d * p : 0.0f) : 0.0f;
+  const bool some = row_max(have ? 1u : 0u) != 0;
+  float g[V] = {};
+  each<0, 16>([&](auto jc) {
+    constexpr int J = decltype(jc)::value;
+    if (J < K) {                                               // wave-uniform
+      const int e = (int)row_lane<J>((uint32_t)id);
+      const float v = __uint_as_float(row_lane<J>(__float_as_uint(mine)));
+      const int at = (e >> 6) * 4 + (e & 3), owner = (e >> 2) & 15;
+      const float add = e >= 0 && owner == l16 ? v : 0.0f;
+#pragma unroll
+      for (int r = 0; r < V; ++r) g[r] += at == r ? add : 0.0f;
+    }
+  });
+  if (dense) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) g[v] = some ? l[v] * inv * (g[v] - dot) : 0.0f;
+  }
+  if (!live) return;
+  T *dst = (T *)args.grad_logits + t * args.ld_grad;
+#pragma unroll
+  for (int c = 0; c < V / 4; ++c) store4<DT>(dst + c * 64 + l16 * 4, E - c * 64 - l16 * 4, g + 4 * c);
+}
+
+// More experts or picks: one wave a token, lanes hold scores and their gradients.
 template <int DT, int R>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteArgs args) {
   typedef typename Val<DT>::type T;
@@ -756,72 +884,53 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteArgs args
   const int64_t t = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
   if (t >= args.tokens) return;
   const T *src = (const T *)args.logits + t * args.ld;
-  float l[R], s[R], ds[R];
-  float top = -INFINITY;
+  int id = lane < K ? args.ids[t * K + lane] : -1;
+  if (id < 0 || id >= E) id = -1;
+  const bool have = id >= 0, dense = !args.sigmoid && !args.renormalize;
+  const float dw = have ? args.grad_weights[t * K + lane] : 0.0f;
+  const float x = have ? Val<DT>::to(src[id]) : 0.0f;
+  float l[R], g[R], inv = 1.0f, p;
+  if (dense) {
+    uint32_t m = 0;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    l[r] = lane + 64 * r < E ? Val<DT>::to(src[lane + 64 * r]) : -INFINITY;
-    top = fmaxf(top, l[r]);
-    ds[r] = 0.0f;
-  }
-  if (args.sigmoid) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) s[r] = 1.0f / (1.0f + expf(-l[r]));
-  } else {
-    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    for (int r = 0; r < R; ++r) {
+      l[r] = lane + 64 * r < E ? Val<DT>::to(src[lane + 64 * r]) : -INFINITY;
+      m = max(m, l[r] == -INFINITY ? 0u : key_of(l[r]));
+    }
+    m = wave_max(m);
+    const float top = m ? value_of(m) : 0.0f;
     float z = 0.0f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      s[r] = l[r] == -INFINITY ? 0.0f : expf(l[r] - top);
-      z += s[r];
+      l[r] = expf(l[r] - top);
+      z += l[r];
     }
-    for (int o = 32; o > 0; o >>= 1) z += __shfl_xor(z, o, 64);
-#pragma unroll
-    for (int r = 0; r < R; ++r) s[r] = z > 0.0f ? s[r] / z : s[r];
+    inv = 1.0f / wave_sum(z);
+    p = have ? expf(x - top) * inv : 0.0f;
+  } else if (args.sigmoid) {
+    p = have ? 1.0f / (1.0f + expf(-x)) : 0.0f;
+  } else {
+    const uint32_t m = wave_max(have ? key_of(x) : 0u);
+    p = have ? expf(x - value_of(m)) : 0.0f;
   }
-  // lane j < K: pick j
-  int id = lane < K ? args.ids[t * K + lane] : -1;
-  if (id >= E) id = -1;
-  float p = 0.0f;
-  const float dw = id >= 0 ? args.grad_weights[t * K + lane] : 0.0f;
+  const float d = pick_gradient(args, have, dw, p, [](float v) { return wave_sum(v); });
+  const float mine = !have ? 0.0f : args.sigmoid ? p * (1.0f - p) * d : dense ? d : p * d;
+  const float dot = dense ? wave_sum(have ? d * p : 0.0f) : 0.0f;
+#pragma unroll
+  for (int r = 0; r < R; ++r) g[r] = 0.0f;
   for (int j = 0; j < K; ++j) {
-    const int i = __shfl(id, j, 64);
-    float v = 0.0f;
+    const int e = __builtin_amdgcn_readlane(id, j);
+    const float v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(mine), j));
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (i == lane + 64 * r) v = s[r];
-    v = __shfl(v, i & 63, 64);
-    if (lane == j && i >= 0) p = v;
+    for (int r = 0; r < R; ++r) g[r] += e == lane + 64 * r ? v : 0.0f;
   }
-  float d = dw;
-  if (args.renormalize) {
-    float total = p, dot = dw * p;
-    for (int o = 32; o > 0; o >>= 1) {
-      total += __shfl_xor(total, o, 64);
-      dot += __shfl_xor(dot, o, 64);
-    }
-    d = (id >= 0 && total > 0.0f) ? (dw - dot / total) / total : 0.0f;
-  }
-  d *= args.scale;
-  float dot = id >= 0 ? d * p : 0.0f;
-  for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, 64);
-  for (int j = 0; j < K; ++j) {
-    const int i = __shfl(id, j, 64);
-    const float v = __shfl(d, j, 64);
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (i == lane + 64 * r) ds[r] += v;
-  }
+  const bool some = __any(have);
   T *dst = (T *)args.grad_logits + t * args.ld_grad;
-  const bool none = __ballot(id >= 0) == 0;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int i = lane + 64 * r;
-    float g;
-    if (args.sigmoid) g = ds[r] == 0.0f ? 0.0f : s[r] * (1.0f - s[r]) * ds[r];
-    else if (args.renormalize) g = ds[r] == 0.0f ? 0.0f : s[r] * ds[r];
-    else g = none ? 0.0f : s[r] * (ds[r] - dot);
-    if (i < E) dst[i] = Val<DT>::from(g);
+    if (dense) g[r] = some ? l[r] * inv * (g[r] - dot) : 0.0f;
+    if (i < E) dst[i] = Val<DT>::from(g[r]);
   }
 }
 
@@ -870,11 +979,17 @@ hipError_t route_for(const RouteArgs &args, hipStream_t s) {
 
 template <int DT>
 hipError_t backward_for(const RouteArgs &args, hipStream_t s) {
-  const dim3 g((unsigned)((args.tokens + kWaves - 1) / kWaves)), b(kThreads);
+  const dim3 b(kThreads);
+  if (args.experts <= 256 && args.top_k <= 16) {
+    const dim3 g((unsigned)((args.tokens + 15) / 16));
+    if (args.experts <= 64) hipLaunchKernelGGL((route_rows_backward_kernel<DT, 4>), g, b, 0, s, args);
+    else if (args.experts <= 128) hipLaunchKernelGGL((route_rows_backward_kernel<DT, 8>), g, b, 0, s, args);
+    else hipLaunchKernelGGL((route_rows_backward_kernel<DT, 16>), g, b, 0, s, args);
+    return hipGetLastError();
+  }
+  const dim3 g((unsigned)((args.tokens + kWaves - 1) / kWaves));
   const int r = (args.experts + 63) / 64;
-  if (r <= 1) hipLaunchKernelGGL((route_backward_kernel<DT, 1>), g, b, 0, s, args);
-  else if (r <= 2) hipLaunchKernelGGL((route_backward_kernel<DT, 2>), g, b, 0, s, args);
-  else if (r <= 4) hipLaunchKernelGGL((route_backward_kernel<DT, 4>), g, b, 0, s, args);
+  if (r <= 4) hipLaunchKernelGGL((route_backward_kernel<DT, 4>), g, b, 0, s, args);
   else if (r <= 8) hipLaunchKernelGGL((route_backward_kernel<DT, 8>), g, b, 0, s, args);
   else hipLaunchKernelGGL((route_backward_kernel<DT, 16>), g, b, 0, s, args);
   return hipGetLastError();
@@ -891,7 +1006,8 @@ hipError_t launch_route(const RouteArgs &args, int dtype, hipStream_t s) {
   if (!args.lists || args.blocks == 1) return e;
   hipLaunchKernelGGL(route_scan_kernel, dim3(args.experts), dim3(kThreads), 0, s, args);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL(route_place_kernel, dim3(args.blocks > 0 ? args.blocks : 1), dim3(kThreads), (size_t)(args.experts + 1) * 4, s, args);
+  const int64_t place = (args.tokens * args.top_k + kPlaceSlots - 1) / kPlaceSlots;
+  hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)(place > 0 ? place : 1)), dim3(kThreads), 0, s, args);
   return hipGetLastError();
 }
 
