@@ -458,27 +458,16 @@ __device__ __forceinline__ float row_sum(float v) {
 template <> __device__ __forceinline__ uint32_t max_over<16>(uint32_t v) { return row_max(v); }
 template <> __device__ __forceinline__ float sum_over<16>(float v) { return row_sum(v); }
 
-constexpr uint32_t kNobody = 0xFFFFu;
+template <int I, int N, typename F>
+__device__ __forceinline__ void each(F &&f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    each<I + 1, N>(f);
+  }
+}
+
 constexpr int kRedo = -2;
 
-// The row's largest key (0: none is left) and the lowest expert that has it,
-// which is taken out.
-template <int V>
-__device__ __forceinline__ uint32_t take_best(uint32_t (&k)[V], int l16, uint32_t &id) {
-  uint32_t m = k[0];
-#pragma unroll
-  for (int v = 1; v < V; ++v) m = max(m, k[v]);
-  m = row_max(m);
-  int at = -1;
-#pragma unroll
-  for (int v = V - 1; v >= 0; --v) at = k[v] == m ? v : at;
-  const uint32_t e = at < 0 ? kNobody : (uint32_t)((at >> 2) * 64 + l16 * 4 + (at & 3));
-  id = row_min(e);
-  at = e == id ? at : -1;
-#pragma unroll
-  for (int v = 0; v < V; ++v) k[v] = at == v ? 0u : k[v];
-  return m;
-}
 // The groups that stay, as a bit at g * p for group g (p lanes share a group),
 // and by how much the last of them is ahead of the first that goes.
 template <typename F, int V>
@@ -526,7 +515,7 @@ __device__ __forceinline__ uint32_t row_groups(const RouteArgs &args, const F (&
 }
 
 template <int DT, int V>
-__global__ __launch_bounds__(512) void route_rows_kernel(RouteArgs args) {
+__global__ __launch_bounds__(512, 4) void route_rows_kernel(RouteArgs args) {
   typedef typename Val<DT>::type T;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int E = args.experts, K = args.top_k;
@@ -541,20 +530,17 @@ __global__ __launch_bounds__(512) void route_rows_kernel(RouteArgs args) {
   // where an expert's group stands, 4 bits a register; the bias's largest
   int p = 1;
   uint32_t shift[(V + 7) / 8] = {};
-  float bias[V], bias_top = 0.0f;
+  float bias_top = 0.0f;
   if (grouped) {
     while (2 * p * args.groups <= 16) p *= 2;
     const int size = E / args.groups;
 #pragma unroll
     for (int v = 0; v < V; ++v) shift[v / 8] |= (uint32_t)(min((v >> 2) * 64 + l16 * 4 + (v & 3), E - 1) / size * p) << (4 * (v & 7));
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = (v >> 2) * 64 + l16 * 4 + (v & 3);
-    bias[v] = biased && e < E ? args.bias[e] : 0.0f;
-    bias_top = fmaxf(bias_top, fabsf(bias[v]));
+  if (biased) {
+    for (int e = l16; e < E; e += 16) bias_top = fmaxf(bias_top, fabsf(args.bias[e]));
+    bias_top = __uint_as_float(row_max(__float_as_uint(bias_top)));
   }
-  if (biased) bias_top = __uint_as_float(row_max(__float_as_uint(bias_top)));
 
   for (int q = wave * 4; q < rows; q += blockDim.x / 16) {       // wave-uniform
     const int mine = q + (lane >> 4);
@@ -574,13 +560,13 @@ __global__ __launch_bounds__(512) void route_rows_kernel(RouteArgs args) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       nan |= l[v] != l[v];
-      mk = max(mk, l[v] == -INFINITY ? 0u : key_of(l[v]));
+      mk = max(mk, key_of(l[v]));
     }
     bool bad = row_max(nan ? 1u : 0u) != 0;
     float top = 0.0f, z = 1.0f;
     if (!args.sigmoid) {
       mk = row_max(mk);
-      top = mk ? value_of(mk) : 0.0f;
+      top = mk != key_of(-INFINITY) ? value_of(mk) : 0.0f;
       bad |= top == INFINITY;                     // inf - inf
       if (biased || grouped || !args.renormalize) {
         z = 0.0f;
@@ -593,10 +579,16 @@ __global__ __launch_bounds__(512) void route_rows_kernel(RouteArgs args) {
     if (grouped || biased) {
       const float largest = args.sigmoid ? 1.0f : 1.0f / z;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float s = args.sigmoid ? __builtin_amdgcn_rcpf(1.0f + exp_fast(-l[v])) : exp_fast(l[v] - top) * largest;
-        c[v] = s + bias[v];
-        if (l[v] == -INFINITY || c[v] != c[v]) c[v] = -INFINITY;
+      for (int i = 0; i < V / 4; ++i) {
+        float b[4] = {};
+        if (biased) load4<kF32>(args.bias + i * 64 + l16 * 4, E - i * 64 - l16 * 4, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int v = 4 * i + j;
+          const float s = args.sigmoid ? __builtin_amdgcn_rcpf(1.0f + exp_fast(-l[v])) : exp_fast(l[v] - top) * largest;
+          c[v] = s + b[j];
+          if (l[v] == -INFINITY || c[v] != c[v]) c[v] = -INFINITY;
+        }
       }
       wanted = lead_wanted(args, largest, bias_top);
     }
@@ -607,49 +599,71 @@ __global__ __launch_bounds__(512) void route_rows_kernel(RouteArgs args) {
       stay = row_groups<float, V>(args, c, (float *)scratch + (threadIdx.x >> 4) * E, p, lane, lead);
       close = !(lead > 2.0f * wanted);          // a score is a sum of two choices
     }
+    // Keys of 24 bits with the expert in the other 8, so that each is its own
+    // and equal ones go to the lower index; 0: out.
     uint32_t k[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const float x = biased ? c[v] : l[v];
-      k[v] = x == -INFINITY || !((stay >> ((shift[v / 8] >> (4 * (v & 7))) & 15)) & 1) ? 0u : key_of(x);
+      const uint32_t e = (uint32_t)((v >> 2) * 64 + l16 * 4 + (v & 3));
+      const uint32_t in = x != -INFINITY ? (stay >> ((shift[v / 8] >> (4 * (v & 7))) & 15)) & 1 : 0u;
+      k[v] = ((key_of(x) & ~255u) | (255u - e)) & (0u - in);
     }
-    // Lane n of the row keeps the n-th pick.  With a bias, each pick's lead over
-    // the next has to pass the 32-bit error, or the two are compared in 64
-    // bits (sigmoids; a softmax needs the whole sum for that), and so has the
-    // last pick's over all that come near it.
-    uint32_t id = kNobody, last = kNobody, before = 0;
+    // Candidates in lane order: the n-th largest key is the largest k - m below
+    // zero (as unsigned numbers, those of the keys under m lie above all
+    // others), so nothing is taken out.  A 16-bit logit fits its key and K
+    // picks are the answer.  Otherwise candidates go on through all that 24
+    // bits, or a choice's 32-bit error, could place above the K-th.
+    const bool fits = DT != kF32 && !biased;
+    uint32_t id = 0x1000u + (uint32_t)l16, m = 0, kth = 0;      // ids past 255: none
     bool open = live && !bad && !close;
-    for (int n = 0; n < E; ++n) {
-      if (!biased && n == K) break;
-      uint32_t e;
-      const uint32_t m = take_best<V>(k, l16, e);
-      if (m == 0) open = false;
-      if (biased && n > 0 && open) {
-        if (value_of(before) - value_of(m) > wanted) {
-          if (n >= K) open = false;
-        } else {
-          const float x = Val<DT>::to(src[last]), y = Val<DT>::to(src[e]);
-          const float bx = args.bias[last], by = args.bias[e];
-          bool ordered = x == y && bx == by && last < e;
-          if (!ordered && args.sigmoid) {
-            const double dx = 1.0 / (1.0 + exp(-(double)x)) + (double)bx, dy = 1.0 / (1.0 + exp(-(double)y)) + (double)by;
-            ordered = dx > dy || (dx == dy && last < e);
-          }
-          if (!ordered) {
-            close = true;
-            open = false;
-          }
-        }
+    for (int n = 0; n <= 16; ++n) {
+      if (fits && n == K) break;
+      uint32_t next = k[0] - m;
+#pragma unroll
+      for (int v = 1; v < V; ++v) next = max(next, k[v] - m);
+      next = row_max(next) + m;
+      if (next == 0) open = false;
+      if (n >= K && open) {
+        const bool below = biased ? value_of(kth & ~255u) - value_of(next | 255u) > wanted : (next >> 8) < (kth >> 8);
+        if (below) open = false;
+        else if (n == 16) close = true;
       }
-      if (open && n < K) {
-        if (l16 == n) id = e;
-        last = e;                                // from the last pick on, all are compared with it
-        before = m;
+      if (open) {
+        if (l16 == n) id = 255u - (next & 255u);
+        if (n == K - 1) kth = next;
+        m = next;
       }
       if (!__any(open)) break;
     }
-    const bool redo = close && live && !bad, have = id != kNobody && !redo;
-    float w = weight_of<16>(args, have, have ? Val<DT>::to(src[id]) : -INFINITY, top, z);
+    float x = id < 256u ? Val<DT>::to(src[id]) : -INFINITY;
+    if (!fits) {
+      // their order by what is compared in earnest: logits, or score + bias in
+      // 64 bits (a softmax's with the 32-bit sum, so its leads have to pass
+      // that sum's error)
+      double y = -INFINITY;
+      if (id < 256u) {
+        if (!biased) y = (double)x;
+        else y = (args.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)top) / (double)z) + (double)args.bias[id];
+      }
+      uint32_t rank = 0;
+      each<1, 16>([&](auto jc) {
+        constexpr int TURN = 0x120 + decltype(jc)::value;      // row_ror
+        const uint32_t e = turned<TURN>(id);
+        const double o = __hiloint2double((int)turned<TURN>((uint32_t)__double2hiint(y)), (int)turned<TURN>((uint32_t)__double2loint(y)));
+        rank += o > y || (o == y && e < id) ? 1 : 0;
+        if (biased && !args.sigmoid) {
+          const float ox = __uint_as_float(turned<TURN>(__float_as_uint(x)));
+          if (e < 256u && id < 256u && fabs(o - y) <= (double)wanted && (o != y || ox != x)) close = true;
+        }
+      });
+      close = row_max(close ? 1u : 0u) != 0;
+      const int to = ((lane & 48) + (int)rank) * 4;             // ranks are a permutation of the row
+      id = (uint32_t)__builtin_amdgcn_ds_permute(to, (int)id);
+      x = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(x)));
+    }
+    const bool redo = close && live && !bad, have = id < 256u && l16 < K && !redo;
+    float w = weight_of<16>(args, have, x, top, z);
     if (bad && live) w = __builtin_nanf("");
     if (mine < rows && l16 < K) {
       const int out = redo ? kRedo : have ? (int)id : -1;
@@ -740,6 +754,16 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(RouteArgs args) {
   static_assert(kRouteMaxExperts <= 4 * kThreads, "four experts a thread");
   __shared__ int offset[kRouteMaxExperts + 1], part[kWaves];
   const int E = args.experts, K = args.top_k, tid = threadIdx.x;
+  const int64_t total = args.tokens * K, first = (int64_t)blockIdx.x * kPlaceSlots + tid;
+  const int slots = args.rows_per_block * K;   // of a block of the first kernel
+  int id[4], at_expert[4];                     // loaded while the offsets are formed
+#pragma unroll
+  for (int i = 0; i < 4; ++i) id[i] = first + i * kThreads < total ? args.ids[first + i * kThreads] : -1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t flat = first + i * kThreads;
+    at_expert[i] = id[i] >= 0 ? args.hist[(int64_t)id[i] * args.blocks + (int)flat / slots] + args.rank[flat] : 0;
+  }
   {
     int v[4], sum = 0, all;
 #pragma unroll
@@ -758,15 +782,12 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(RouteArgs args) {
   __syncthreads();
   if (blockIdx.x == 0)
     for (int i = tid; i <= E; i += kThreads) args.offsets[i] = offset[i];
-  const int64_t total = args.tokens * K;
-  const int slots = args.rows_per_block * K;   // of a block of the first kernel
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t flat = (int64_t)blockIdx.x * kPlaceSlots + i * kThreads + tid;
+    const int64_t flat = first + i * kThreads;
     if (flat >= total) break;
-    const int id = args.ids[flat];
-    if (id >= 0) {
-      const int place = offset[id] + args.hist[(int64_t)id * args.blocks + (int)flat / slots] + args.rank[flat];
+    if (id[i] >= 0) {
+      const int place = offset[id[i]] + at_expert[i];
       args.order[place] = (int)flat;
       args.rows[place] = (int)flat / K;
     }
@@ -774,18 +795,10 @@ __global__ __launch_bounds__(kThreads) void route_place_kernel(RouteArgs args) {
   }
 }
 
-// Sums over a row of 16 lanes and broadcasts from its lane J, in every lane
+// The value of the row's lane J, in every lane
 template <int J>
 __device__ __forceinline__ uint32_t row_lane(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x150 + J, 0xF, 0xF, true);
-}
-
-template <int I, int N, typename F>
-__device__ __forceinline__ void each(F &&f) {
-  if constexpr (I < N) {
-    f(std::integral_constant<int, I>{});
-    each<I + 1, N>(f);
-  }
 }
 
 // Gradient of the weights.  With p_j the taken scores and d_j the gradient of

@@ -40,7 +40,7 @@ def _matrix(t, name, shape=None, dtype=None, device=None) -> int:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
     if t.dim() != 2:
         raise ValueError("%s must be 2-D" % name)
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if dtype is not None:
         if t.dtype != dtype:
@@ -61,20 +61,29 @@ def _flat(t, name, shape, dtype, device) -> int:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
     if t.dtype != dtype:
         raise ValueError("%s must be %s (got %s)" % (name, dtype, t.dtype))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return t.data_ptr()
 
 
+# torch's current stream and device as plain numbers (a Stream object costs
+# more than a small call's launch)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _call(device, fn, *args) -> None:
     """fn(*args, stream) with the tensors' device current."""
-    if device.index == torch.cuda.current_device():
-        _lib.check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
-        return
-    with torch.cuda.device(device):
-        _lib.check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    index = device.index
+    if index == _current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        _lib.check(status)
 
 
 def _workspace(workspace, need, device) -> torch.Tensor:
@@ -117,8 +126,13 @@ class Checkpoint:
     def empty(cls, rows: int, cols: int, format: str = "e4m3", device="cuda") -> "Checkpoint":
         if cols < 1:
             raise ValueError("cols must be >= 1")
-        return cls(torch.empty(rows, -(-cols // 16) * 16, dtype=torch.uint8, device=device),
-                   torch.empty(rows, -(-cols // BLOCK), dtype=torch.uint8, device=device), cols, format)
+        if format not in _FORMATS:
+            raise ValueError("format must be one of %s (got %r)" % (sorted(_FORMATS), format))
+        self = object.__new__(cls)
+        self.codes = torch.empty(rows, -(-cols // 16) * 16, dtype=torch.uint8, device=device)
+        self.scales = torch.empty(rows, -(-cols // BLOCK), dtype=torch.uint8, device=device)
+        self.cols, self.format = cols, format
+        return self
 
     @property
     def shape(self):
@@ -142,9 +156,9 @@ class Checkpoint:
 def _saved(ckpt, name, shape=None, device=None) -> Checkpoint:
     if not isinstance(ckpt, Checkpoint):
         raise TypeError("%s must be a Checkpoint" % name)
-    if shape is not None and ckpt.shape != tuple(shape):
+    if shape is not None and (ckpt.codes.shape[0] != shape[0] or ckpt.cols != shape[1]):
         raise ValueError("%s has shape %s, expected %s" % (name, ckpt.shape, tuple(shape)))
-    if device is not None and ckpt.device != device:
+    if device is not None and ckpt.codes.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, ckpt.device, device))
     return ckpt
 
@@ -152,7 +166,7 @@ def _saved(ckpt, name, shape=None, device=None) -> Checkpoint:
 def _output(out, name, shape, dtype, device):
     """(tensor, row stride) of a matrix output, allocated if None."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device), shape[1]
+        return torch.empty(shape[0], shape[1], dtype=dtype, device=device), shape[1]
     return out, _matrix(out, name, shape, dtype, device)
 
 
@@ -163,9 +177,9 @@ def checkpoint_pack(x: torch.Tensor, *, format: str = "e4m3", out: Optional[Chec
     ld = _matrix(x, "x")
     if out is None:
         out = Checkpoint.empty(x.shape[0], x.shape[1], format, x.device)
-    _saved(out, "out", x.shape, x.device)
-    rec = out._record()
-    _call(x.device, _lib.load().muon_ckpt_pack, x.data_ptr(), ld, _DT[x.dtype], rec)
+    else:
+        _saved(out, "out", x.shape, x.device)
+    _call(x.device, _lib.load().muon_ckpt_pack, x.data_ptr(), ld, _DT[x.dtype], out._record())
     return out
 
 
@@ -275,21 +289,10 @@ class Routing(NamedTuple):
     rows: Optional[torch.Tensor]
 
 
-def _routing(logits, ld, top_k, score, renormalize, scale):
+def _score(score) -> int:
     if score not in _SCORES:
         raise ValueError("score must be one of %s (got %r)" % (sorted(_SCORES), score))
-    a = _lib.MuonRouting()
-    a.logits = logits.data_ptr()
-    a.ld_logits = ld
-    a.tokens, a.experts = logits.shape
-    a.dtype = _DT[logits.dtype]
-    a.top_k = top_k
-    a.score = _SCORES[score]
-    a.groups = a.top_groups = 1
-    a.group_top = 2
-    a.renormalize = int(renormalize)
-    a.scale = scale
-    return a
+    return _SCORES[score]
 
 
 def route(logits: torch.Tensor, top_k: int, *, bias: Optional[torch.Tensor] = None, score: str = "softmax", groups: int = 1,
@@ -309,32 +312,30 @@ def route(logits: torch.Tensor, top_k: int, *, bias: Optional[torch.Tensor] = No
     device = logits.device
     tokens, experts = logits.shape
     top_k = int(top_k)
-    if experts < 1:
-        raise ValueError("logits must have at least one expert")
-    a = _routing(logits, ld, top_k, score, renormalize, scale)
-    a.groups, a.top_groups, a.group_top = groups, top_groups, group_top
+    if experts < 1 or top_k < 1:
+        raise ValueError("logits must have at least one expert, and top_k be at least 1")
+    code = _score(score)
+    bias_at = mask_at = load_at = None
     if bias is not None:
-        a.bias = _flat(bias, "bias", (experts,), torch.float32, device)
+        bias_at = _flat(bias, "bias", (experts,), torch.float32, device)
     if token_mask is not None:
-        if token_mask.dtype != torch.bool:
-            _flat(token_mask, "token_mask", (tokens,), torch.uint8, device)
-        a.token_mask = _flat(token_mask, "token_mask", (tokens,), token_mask.dtype, device)
+        mask_at = _flat(token_mask, "token_mask", (tokens,), torch.bool if token_mask.dtype == torch.bool else torch.uint8, device)
     if load is not None:
-        a.load = _flat(load, "load", (experts,), torch.int64, device)
-    if top_k < 1:
-        raise ValueError("top_k must be >= 1")
+        load_at = _flat(load, "load", (experts,), torch.int64, device)
     ids = torch.empty(tokens, top_k, dtype=torch.int32, device=device)
     weights = torch.empty(tokens, top_k, dtype=torch.float32, device=device)
-    a.expert_ids, a.weights = ids.data_ptr(), weights.data_ptr()
     counts = offsets = order = rows = None
+    lists = (None, None, None, None)
     if dispatch:
         counts = torch.empty(experts, dtype=torch.int32, device=device)
         offsets = torch.empty(experts + 1, dtype=torch.int32, device=device)
         order = torch.empty(tokens * top_k, dtype=torch.int32, device=device)
         rows = torch.empty(tokens * top_k, dtype=torch.int32, device=device)
-        a.counts, a.offsets, a.order, a.rows = counts.data_ptr(), offsets.data_ptr(), order.data_ptr(), rows.data_ptr()
+        lists = (counts.data_ptr(), offsets.data_ptr(), order.data_ptr(), rows.data_ptr())
+    args = _lib.MuonRouting(logits.data_ptr(), ld, tokens, _DT[logits.dtype], experts, top_k, code, groups, top_groups, group_top,
+                            1 if renormalize else 0, scale, bias_at, mask_at, ids.data_ptr(), weights.data_ptr(), *lists, load_at)
     lib = _lib.load()
-    ref = ctypes.byref(a)
+    ref = ctypes.byref(args)
     ws = _workspace(workspace, _size(lib.muon_route_workspace_size(ref)), device)
     _call(device, lib.muon_route, ref, ws.data_ptr(), ws.numel())
     return Routing(ids, weights, counts, offsets, order, rows)
@@ -347,15 +348,16 @@ def route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, experts: to
     are tokens x top_k.  The choice itself carries no gradient."""
     ld = _matrix(logits, "logits")
     device = logits.device
-    tokens = logits.shape[0]
+    tokens, width = logits.shape
     if not isinstance(experts, torch.Tensor) or experts.dim() != 2:
         raise ValueError("experts must be a tensor of tokens x top_k")
     top_k = experts.shape[1]
-    a = _routing(logits, ld, top_k, score, renormalize, scale)
-    a.expert_ids = _flat(experts, "experts", (tokens, top_k), torch.int32, device)
+    ids = _flat(experts, "experts", (tokens, top_k), torch.int32, device)
     dw = _flat(grad_weights, "grad_weights", (tokens, top_k), torch.float32, device)
-    out, ld_out = _output(out, "out", tuple(logits.shape), logits.dtype, device)
-    _call(device, _lib.load().muon_route_backward, ctypes.byref(a), dw, out.data_ptr(), ld_out)
+    args = _lib.MuonRouting(logits.data_ptr(), ld, tokens, _DT[logits.dtype], width, top_k, _score(score), 1, 1, 2,
+                            1 if renormalize else 0, scale, None, None, ids)
+    out, ld_out = _output(out, "out", (tokens, width), logits.dtype, device)
+    _call(device, _lib.load().muon_route_backward, ctypes.byref(args), dw, out.data_ptr(), ld_out)
     return out
 
 
