@@ -128,6 +128,7 @@ muon_status check_pair(const muon_ckpt *a, const muon_ckpt *b) {
 
 struct WgradPlan {
   int wide = 0;            // WgradArgs::wide
+  double time = 1e30;      // estimate
   int64_t tiles_n = 0, tiles_d = 0;
   int splits = 1;          // parts of the token range
   int64_t split_len = 0;
@@ -155,24 +156,13 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int kWideBlocks = 512;               // two a CU
 constexpr int64_t kWidePart = int64_t(256) * 128 * 4;
 
-// 128 x 128 tiles of one matrix: the token range is cut into parts so that the
-// blocks fill the chip; the parts are joined in order.
-void plan_parts(const muon_wgrad *a, WgradPlan &p) {
-  const int64_t want = std::min<int64_t>(ceil_div(512, p.tiles_n * p.tiles_d), a->slots / 256);
-  if (a->offsets || want <= 1) return;
-  p.split_len = ceil_div(ceil_div(a->slots, want), kWgradK) * kWgradK;
-  p.splits = (int)ceil_div(a->slots, p.split_len);
-  if (p.splits > 1) p.bytes = (size_t)p.splits * (size_t)(a->outs * a->ckpt.cols) * 4;
-}
-
-// Wide tiles.  One matrix: each number of parts' time is estimated and the
-// best is taken.  A round of 512 pieces takes 1.0 us a step, one of at most
-// 256 (a block alone on its CU) 0.6; filling a block and storing a piece take
-// ten steps more; partials pass memory twice at 4.5 TB/s and their join costs
-// a launch.
+// Wide tiles.  Each number of parts' time is estimated and the best is taken.
+// A round of 512 pieces takes 1.0 us a step, one of at most 256 (a block alone
+// on its CU) 0.6; filling a block and storing a piece take ten steps more;
+// partials pass memory twice at 4.5 TB/s and their join costs a launch.
 bool plan_wide(const muon_wgrad *a, WgradPlan &p) {
-  const int64_t N = a->outs, D = a->ckpt.cols;
-  if (N <= 64 || D <= 64 || N % 8 != 0 || a->slots == 0 || a->ckpt.rows == 0) return false;
+  const int64_t N = a->outs, D = a->ckpt.cols, E = a->experts;
+  if (N % 8 != 0 || a->slots == 0 || a->ckpt.rows == 0) return false;
   const int64_t waste1 = ceil_div(N, 256) * 256 * ceil_div(D, 128) * 128, waste2 = ceil_div(N, 128) * 128 * ceil_div(D, 256) * 256;
   // (int8 codes keep to one chunk a thread: two fill the registers past 256,
   // 2048 x 1408 x 64 experts 532 us against 400 with 9% more padding)
@@ -180,34 +170,50 @@ bool plan_wide(const muon_wgrad *a, WgradPlan &p) {
   p.tiles_n = ceil_div(N, p.wide == 1 ? 256 : 128);
   p.tiles_d = ceil_div(D, p.wide == 2 ? 256 : 128);
   const int64_t tiles = p.tiles_n * p.tiles_d;
-  if (tiles * std::max<int64_t>(a->experts, 64) >= (int64_t(1) << 30)) return false;
-  if (a->offsets) return true;
-  double best = 1e30;
-  for (int64_t s = 1; s <= 64; ++s) {
+  if (tiles * std::max<int64_t>(E, 64) >= (int64_t(1) << 30)) return false;
+  for (int64_t s = 1; s <= (a->offsets ? 1 : 64); ++s) {
     const int64_t len = ceil_div(ceil_div(a->slots, s), 2 * kWgradK) * 2 * kWgradK;
     if (ceil_div(a->slots, len) != s) continue;
-    const int64_t items = tiles * s, rounds = ceil_div(items, kWideBlocks);
-    const double per_step = items <= kWideBlocks / 2 ? 0.6e-6 : 1.0e-6;
-    double t = (double)rounds * ((double)(len / kWgradK) + 10) * per_step;
+    const int64_t items = tiles * s * E;
+    const double rounds = items <= kWideBlocks ? 1.0 : std::max((double)items / kWideBlocks, 1.0), steps = (double)len / kWgradK / (double)E;
+    const double whole = a->offsets ? rounds : (double)ceil_div(items, kWideBlocks);
+    double t = whole * (steps + 10) * (items <= kWideBlocks / 2 ? 0.6e-6 : 1.0e-6);
     if (s > 1) t += (double)(items * kWidePart) * 2 / 4.5e12 + 4e-6;
-    if (t < best) best = t, p.splits = (int)s, p.split_len = len;
+    if (t < p.time) p.time = t, p.splits = (int)s, p.split_len = len;
   }
   if (p.splits > 1) p.bytes = (size_t)(p.splits * tiles) * (size_t)kWidePart;
   return true;
 }
 
+// 64 x 64 tiles, four waves that share a block's steps, three blocks a CU:
+// near 1.5 us to start and store a round, 0.45 us a wave's step.
+void plan_near(const muon_wgrad *a, WgradPlan &p) {
+  const int64_t E = a->experts;
+  p.tiles_n = ceil_div(a->outs, 64);
+  p.tiles_d = ceil_div(a->ckpt.cols, 64);
+  const int64_t tiles = p.tiles_n * p.tiles_d;
+  for (int64_t s = 1; s <= (a->offsets || a->slots == 0 ? 1 : 64); ++s) {
+    const int64_t len = std::max<int64_t>(ceil_div(ceil_div(a->slots, s), 4 * kWgradK), 1) * 4 * kWgradK;
+    if (s > 1 && ceil_div(a->slots, len) != s) continue;
+    const int64_t blocks = tiles * s * E;
+    const double rounds = std::max((double)blocks / 768, 1.0);
+    double t = rounds * ((double)ceil_div(ceil_div(len, E), 4 * kWgradK) * 0.45e-6 + 1.5e-6) + 2e-6;
+    if (s > 1) t += (double)(tiles * s) * 64 * 64 * 8 / 4.5e12 + 3e-6;
+    if (t < p.time) p.time = t, p.splits = (int)s, p.split_len = len;
+  }
+  if (p.splits > 1) p.bytes = (size_t)(p.splits * tiles) * 64 * 64 * 4;
+}
+
 WgradPlan plan_wgrad(const muon_wgrad *a) {
-  WgradPlan wide, p;
+  WgradPlan wide, near;
   const bool fits = plan_wide(a, wide);
-  p.tiles_n = ceil_div(a->outs, kWgradTile);
-  p.tiles_d = ceil_div(a->ckpt.cols, kWgradTile);
-  plan_parts(a, p);
+  plan_near(a, near);
   // the size covers both, whatever grad_y's address and strides allow
-  const size_t bytes = align256(std::max(fits ? wide.bytes : 0, p.bytes));
+  const size_t bytes = align256(std::max(fits ? wide.bytes : 0, near.bytes));
   const bool aligned = a->ld_grad_y % 8 == 0 && (((uintptr_t)a->grad_y) & 15) == 0 && a->ld_grad_y <= (1 << 24) &&
                        a->ckpt.codes_ld <= (1 << 25) && a->ckpt.scales_ld <= (1 << 25) &&
                        (!a->rows_of || a->ckpt.rows * std::max(a->ckpt.codes_ld, a->ckpt.scales_ld) < (int64_t(1) << 32) - 1);
-  if (fits && aligned) p = wide;
+  WgradPlan p = fits && aligned && wide.time < near.time ? wide : near;
   p.bytes = bytes;
   return p;
 }
@@ -415,8 +421,7 @@ muon_status muon_ckpt_wgrad(const muon_wgrad *args, void *workspace, size_t work
   a.out_dtype = (int32_t)w.out_dtype;
   a.accumulate = w.accumulate != 0;
   a.transposed = w.transposed != 0;
-  hipError_t e = launch_wgrad(a, (int)w.dtype, (int)w.ckpt.format, (hipStream_t)stream);
-  if (e == hipSuccess && !p.wide && p.splits > 1) e = launch_wgrad_join(a, (hipStream_t)stream);
+  const hipError_t e = launch_wgrad(a, (int)w.dtype, (int)w.ckpt.format, (hipStream_t)stream);
   return launched(e, "muon_ckpt_wgrad");
 }
 

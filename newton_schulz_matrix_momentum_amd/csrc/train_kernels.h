@@ -75,15 +75,13 @@ struct WgradArgs {
   int32_t out_dtype;
   int32_t accumulate;
   int32_t transposed;
-  int32_t wide;            // 0: 128 x 128 tiles; 1: 256 outs x 128 columns; 2: 128 x 256
+  int32_t wide;            // 0: 64 x 64 tiles; 1: 256 outs x 128 columns; 2: 128 x 256
   int32_t blocks, items;   // wide: blocks of the launch; tiles x experts or parts, which the blocks take in turn
   FastDiv tiles, div_d;    // wide: by the tiles of a matrix, and by tiles_d
 };
-constexpr int kWgradTile = 128;
 constexpr int kWgradK = 32;
 
 hipError_t launch_wgrad(const WgradArgs &args, int dtype, int format, hipStream_t s);
-hipError_t launch_wgrad_join(const WgradArgs &args, hipStream_t s);
 
 // ---------------------------------------------------------------- routing
 constexpr int kRouteMaxExperts = 1024;

@@ -121,142 +121,13 @@ __device__ __forceinline__ void put4_any(void *out, int dtype, int64_t at, int n
   else put4<kF16>(out, at, n, vec, acc, v);
 }
 
-// 128 outs x 128 columns per block of four waves (64 x 64 each), 32 tokens a
-// step, double-buffered through registers.
-//
-// LDS rows hold one token's 128 values, 256 bytes; the 32-byte chunk c of row
-// r is kept at c ^ key(r): the 8 rows that half a wave reads at once (a
-// 16-lane group takes 4 rows) have distinct keys, so their equal chunks fall
-// into distinct banks.
 constexpr int kThreads = 256;
-constexpr int kRowBytes = kWgradTile * 2;
+
+// LDS rows of a wide tile hold one token's values of one operand; the 32-byte
+// chunk c of row r is kept at c ^ key(r): the 8 rows that half a wave reads at
+// once (a 16-lane group takes 4 rows) have distinct keys, so their equal
+// chunks fall into distinct banks.
 __device__ __forceinline__ int key(int r) { return (r & 3) | ((r >> 1) & 4); }
-
-template <int DT, int FMT, bool TRANS>
-__global__ __launch_bounds__(kThreads, 2) void wgrad_kernel(WgradArgs args) {
-  typedef typename Val<DT>::type T;
-  __shared__ __attribute__((aligned(16))) char lds[2][2][kWgradK * kRowBytes];   // [buffer][dy, x^]
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wn = wave >> 1, wd = wave & 1;
-  const int tn = blockIdx.x / args.tiles_d, td = blockIdx.x % args.tiles_d;
-  const int e = blockIdx.y;
-  int64_t lo, hi;
-  slot_range(args, e, lo, hi);
-  if (args.splits > 1) {
-    lo += blockIdx.z * args.split_len;
-    hi = min(hi, lo + args.split_len);
-  }
-  const int n0 = tn * kWgradTile, d0 = td * kWgradTile;
-
-  // dy: thread covers tokens tid / 16 and 16 + tid / 16, 8 columns from 8 (tid % 16)
-  const int y_row = tid >> 4, y_col = (tid & 15) * 8;
-  const int y_n = min(args.outs - (n0 + y_col), 8);
-  // x^: thread covers token tid / 8, 16 columns from 16 (tid % 8)
-  const int x_row = tid >> 3, x_col = (tid & 7) * 16;
-  const bool x_in = d0 + x_col < args.cols;
-  const T *dy = (const T *)args.dy + n0 + y_col;
-  const uint8_t *codes = args.codes + d0 + x_col;
-  const uint8_t *scales = args.scales + (d0 + x_col) / kCkptBlock;
-
-  u32x4 ry[2], rx = {};
-  uint32_t rb = 0;
-  auto fetch = [&](int64_t base) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t slot = base + y_row + 16 * i;
-      ry[i] = u32x4{};
-      if (row_of(args, slot, hi) >= 0 && y_n > 0) {
-        const T *p = dy + slot * args.ld_dy;
-        if (y_n == 8) {
-          ry[i] = *(const u32x4u *)p;
-        } else {
-          uint16_t t[8] = {};
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < y_n) t[k] = __builtin_bit_cast(uint16_t, p[k]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ry[i][k] = (uint32_t)t[2 * k] | ((uint32_t)t[2 * k + 1] << 16);
-        }
-      }
-    }
-    const int64_t r = row_of(args, base + x_row, hi);
-    rx = u32x4{};
-    rb = 127;
-    if (r >= 0 && x_in) {
-      rx = *(const u32x4 *)(codes + r * args.codes_ld);
-      rb = scales[r * args.scales_ld];
-    }
-  };
-  auto stage = [&](int buf) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = y_row + 16 * i, c = (tid & 15) >> 1;
-      *(u32x4 *)(&lds[buf][0][r * kRowBytes + ((c ^ key(r)) * 32) + (tid & 1) * 16]) = ry[i];
-    }
-    u32x4 a, b;
-    decode16<DT, FMT>(rx, rb, a, b);
-    char *p = &lds[buf][1][x_row * kRowBytes + (((tid & 7) ^ key(x_row)) * 32)];
-    *(u32x4 *)p = a;
-    *(u32x4 *)(p + 16) = b;
-  };
-  // fragment of 16 columns from 16 c: tokens 8 g .. 8 g + 7 of the lane's column
-  const int g = lane >> 4, j = lane & 15;
-  auto frag = [&](const char *t, int c) {
-    const int r0 = 8 * g + (j >> 2), r1 = r0 + 4;
-    const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) i16x4 *)(t + r0 * kRowBytes + ((c ^ key(r0)) * 32) + (j & 3) * 8));
-    const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) i16x4 *)(t + r1 * kRowBytes + ((c ^ key(r1)) * 32) + (j & 3) * 8));
-    const uint2 a = __builtin_bit_cast(uint2, x), b = __builtin_bit_cast(uint2, y);
-    return u32x4{a.x, a.y, b.x, b.y};
-  };
-
-  // acc[i][k]: the MFMA's rows are the index that is contiguous in the output
-  f32x4 acc[4][4] = {};
-  if (lo < hi) {
-    fetch(lo);
-    stage(0);
-    __syncthreads();
-    int buf = 0;
-    for (int64_t base = lo; base < hi; base += kWgradK) {
-      const bool more = base + kWgradK < hi;
-      if (more) fetch(base + kWgradK);
-      u32x4 fy[4], fx[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        fy[i] = frag(lds[buf][0], wn * 4 + i);
-        fx[i] = frag(lds[buf][1], wd * 4 + i);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if constexpr (TRANS) mma<DT>(fy[i], fx[k], acc[i][k]);
-          else mma<DT>(fx[i], fy[k], acc[i][k]);
-        }
-      if (more) stage(buf ^ 1);
-      __syncthreads();
-      buf ^= 1;
-    }
-  }
-
-  const int rows = TRANS ? args.cols : args.outs, width = TRANS ? args.outs : args.cols;
-  const int row_base = TRANS ? d0 + wd * 64 : n0 + wn * 64, col_base = TRANS ? n0 + wn * 64 : d0 + wd * 64;
-  const int64_t size = (int64_t)args.outs * args.cols;
-  const bool split = args.splits > 1;
-  const int ot = split ? (int)kF32 : args.out_dtype;
-  const bool vec = (width & 3) == 0 && (((uintptr_t)(split ? (void *)args.part : args.out)) & 15) == 0;
-  const int64_t first = (split ? (int64_t)blockIdx.z : (int64_t)e) * size;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int row = row_base + 16 * k + (lane & 15), col = col_base + 16 * i + 4 * (lane >> 4);
-      if (row < rows && col < width)
-        put4_any(split ? (void *)args.part : args.out, ot, first + (int64_t)row * width + col, min(width - col, 4), vec,
-                 !split && args.accumulate, acc[i][k]);
-    }
-}
 
 // Output row and first of 4 consecutive columns of accumulator (i, k) of a wide
 // tile: the MFMA's rows (4 consecutive a lane) are contiguous in the output.
@@ -797,25 +668,187 @@ __global__ __launch_bounds__(kThreads) void wgrad_wide_join_kernel(WgradArgs arg
     put4_any(args.out, args.out_dtype, (int64_t)r * width + c, min(width - c, 4), (width & 3) == 0 && (((uintptr_t)args.out) & 15) == 0, args.accumulate, v);
 }
 
-// 128 x 128 tiles: out = (out +) the sum of the parts, in their order
-__global__ __launch_bounds__(256) void wgrad_join_kernel(WgradArgs args) {
-  const int64_t size = (int64_t)args.outs * args.cols;
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (at >= size) return;
-  const int n = (int)min(size - at, (int64_t)4);
-  f32x4 v = {};
-  const bool vec = (size & 3) == 0;
-  for (int p = 0; p < args.splits; ++p) {
-    const float *src = args.part + p * size + at;
-    if (vec) {
-      v += *(const f32x4 *)src;
-    } else {
+// ---------------------------------------------------------------------------
+// Small matrices, few tokens, and rows that the wide tiles' DMA cannot read
+// (odd widths, unaligned strides): 64 outs x 64 columns per block.  The block's
+// four waves take its steps of 32 tokens in turn, each for the whole tile, in
+// LDS of its own, so the loop has no barrier: rows go global -> registers ->
+// LDS, fragments come back through transposing reads, and the next step's
+// rows are on their way meanwhile.  The waves' sums meet in LDS at the end
+// ((0 + 2) + (1 + 3)).  Many small blocks hide the latency that bounds this.
+//
+// LDS rows are 128 bytes; the 32-byte chunk c of row r is kept at c ^ near_key(r):
+// of the 8 rows that half a wave reads at once, the four of equal parity have
+// distinct keys.
+constexpr int kNear = 64;
+__device__ __forceinline__ int near_key(int r) { return ((r >> 1) & 1) | ((r >> 2) & 2); }
+
+// output row and first of 4 columns of accumulator (i, k)
+template <bool TRANS>
+__device__ __forceinline__ void near_place(int n0, int d0, int lane, int f, int &r, int &c) {
+  // i: the MFMA's rows, contiguous in the output; k: its columns
+  const int i = f >> 2, k = f & 3;
+  r = (TRANS ? d0 : n0) + 16 * k + (lane & 15);
+  c = (TRANS ? n0 : d0) + 16 * i + 4 * (lane >> 4);
+}
+
+template <int DT, int FMT, bool TRANS>
+__global__ __launch_bounds__(kThreads, 3) void wgrad_near_kernel(WgradArgs args) {
+  typedef typename Val<DT>::type T;
+  constexpr int ROW = kNear * 2, STAGE = kWgradK * ROW;          // 4 KB an operand
+  __shared__ __attribute__((aligned(16))) char lds[4 * 2 * STAGE];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tn = blockIdx.x / args.tiles_d, td = blockIdx.x % args.tiles_d;
+  const int n0 = tn * kNear, d0 = td * kNear;
+  int64_t lo, hi;
+  slot_range(args, blockIdx.y, lo, hi);
+  if (args.splits > 1) {
+    lo += blockIdx.z * args.split_len;
+    hi = min(hi, lo + args.split_len);
+  }
+  char *const ybuf = lds + wave * 2 * STAGE, *const xbuf = ybuf + STAGE;
+
+  // dy: lane covers row lane / 8 + 8 i, 8 columns from 8 (lane % 8)
+  const int y_row = lane >> 3, y_col = (lane & 7) * 8;
+  const int y_n = min(args.outs - (n0 + y_col), 8);
+  const T *dy = (const T *)args.dy + n0 + y_col;
+  // x^: lane covers row lane / 4 + 16 i, 16 columns from 16 (lane % 4)
+  const int x_row = lane >> 2, x_col = (lane & 3) * 16;
+  const bool x_in = d0 + x_col < args.cols;
+  const uint8_t *codes = args.codes + d0 + x_col, *scales = args.scales + (d0 + x_col) / kCkptBlock;
+  u32x4 ry[4], rx[2];
+  uint32_t rb[2];
+  auto fetch = [&](int64_t base) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n) v[i] += src[i];
+    for (int i = 0; i < 4; ++i) {
+      const int64_t slot = base + y_row + 8 * i;
+      ry[i] = u32x4{};
+      if (y_n > 0 && row_of(args, slot, hi) >= 0) {
+        const T *p = dy + slot * args.ld_dy;
+        if (y_n == 8) {
+          ry[i] = *(const u32x4u *)p;
+        } else {
+          uint16_t t[8] = {};
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < y_n) t[k] = __builtin_bit_cast(uint16_t, p[k]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ry[i][k] = (uint32_t)t[2 * k] | ((uint32_t)t[2 * k + 1] << 16);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t r = row_of(args, base + x_row + 16 * i, hi);
+      rx[i] = u32x4{};
+      rb[i] = 127;
+      if (r >= 0 && x_in) {
+        rx[i] = *(const u32x4 *)(codes + r * args.codes_ld);
+        rb[i] = scales[r * args.scales_ld];
+      }
+    }
+  };
+  auto stage = [&]() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = y_row + 8 * i;
+      *(u32x4 *)(ybuf + r * ROW + ((((lane & 7) >> 1) ^ near_key(r)) * 32) + (lane & 1) * 16) = ry[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = x_row + 16 * i;
+      u32x4 a, b;
+      decode16<DT, FMT>(rx[i], rb[i], a, b);
+      char *p = xbuf + r * ROW + (((lane & 3) ^ near_key(r)) * 32);
+      *(u32x4 *)p = a;
+      *(u32x4 *)(p + 16) = b;
+    }
+  };
+  const int r0 = 8 * (lane >> 4) + ((lane & 15) >> 2);          // near_key(r0 + 4) is near_key(r0)
+  auto frag = [&](const char *t, int c) {
+    const char *p = t + r0 * ROW + ((c ^ near_key(r0)) * 32) + (lane & 3) * 8;
+    const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4 *)p);
+    const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4 *)(p + 4 * ROW));
+    const uint2 a = __builtin_bit_cast(uint2, x), b = __builtin_bit_cast(uint2, y);
+    return u32x4{a.x, a.y, b.x, b.y};
+  };
+
+  f32x4 acc[16] = {};
+  int64_t base = lo + wave * kWgradK;
+  if (base < hi) fetch(base);
+  for (; base < hi; base += 4 * kWgradK) {                       // wave-uniform
+    stage();
+    if (base + 4 * kWgradK < hi) fetch(base + 4 * kWgradK);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    u32x4 fy[4], fx[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fy[i] = frag(ybuf, i), fx[i] = frag(xbuf, i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (TRANS) mma<DT>(fy[i], fx[k], acc[4 * i + k]);
+        else mma<DT>(fx[i], fy[k], acc[4 * i + k]);
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+
+  // the waves' sums, 16 KB each, in the two halves of LDS
+  f32x4 *const half = (f32x4 *)lds + (wave & 1) * 16 * 64;
+  __syncthreads();
+  if (wave >= 2) {
+#pragma unroll
+    for (int f = 0; f < 16; ++f) half[f * 64 + lane] = acc[f];
+  }
+  __syncthreads();
+  if (wave < 2) {
+#pragma unroll
+    for (int f = 0; f < 16; ++f) {
+      acc[f] += half[f * 64 + lane];
+      half[f * 64 + lane] = acc[f];
     }
   }
-  put4_any(args.out, args.out_dtype, at, n, (((uintptr_t)args.out) & 15) == 0, args.accumulate, v);
+  __syncthreads();
+  const int rows = TRANS ? args.cols : args.outs, width = TRANS ? args.outs : args.cols;
+  const bool split = args.splits > 1;
+  const bool vec = (width & 3) == 0 && (((uintptr_t)args.out) & 15) == 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int f = 4 * wave + q;
+    const f32x4 v = ((f32x4 *)lds)[f * 64 + lane] + ((f32x4 *)lds)[(16 + f) * 64 + lane];
+    if (split) {
+      *(f32x4 *)(args.part + ((((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * 16 + f) * 64 + lane) * 4) = v;
+      continue;
+    }
+    int r, c;
+    near_place<TRANS>(n0, d0, lane, f, r, c);
+    if (r < rows && c < width)
+      put4_any(args.out, args.out_dtype, (int64_t)blockIdx.y * args.outs * args.cols + (int64_t)r * width + c, min(width - c, 4), vec, args.accumulate, v);
+  }
+}
+
+// out = (out +) the sum of the parts, in their order: a wave a fragment of a tile
+template <bool TRANS>
+__global__ __launch_bounds__(kThreads) void wgrad_near_join_kernel(WgradArgs args) {
+  const int tiles = args.tiles_n * args.tiles_d, lane = threadIdx.x & 63;
+  const int t = blockIdx.x / 4, f = (blockIdx.x % 4) * 4 + (threadIdx.x >> 6);
+  const float *src = args.part + (((int64_t)t * 16 + f) * 64 + lane) * 4;
+  f32x4 v = {};
+  int p = 0;
+  for (; p + 4 <= args.splits; p += 4) {        // four loads on their way
+    f32x4 a[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = *(const f32x4 *)(src + (int64_t)(p + i) * tiles * 16 * 256);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v += a[i];
+  }
+  for (; p < args.splits; ++p) v += *(const f32x4 *)(src + (int64_t)p * tiles * 16 * 256);
+  const int rows = TRANS ? args.cols : args.outs, width = TRANS ? args.outs : args.cols;
+  int r, c;
+  near_place<TRANS>(t / args.tiles_d * kNear, t % args.tiles_d * kNear, lane, f, r, c);
+  if (r < rows && c < width)
+    put4_any(args.out, args.out_dtype, (int64_t)r * width + c, min(width - c, 4), (width & 3) == 0 && (((uintptr_t)args.out) & 15) == 0, args.accumulate, v);
 }
 
 }  // namespace
@@ -849,16 +882,20 @@ hipError_t launch_wide(const WgradArgs &args, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int DT, int FMT>
+hipError_t launch_near(const WgradArgs &args, hipStream_t s) {
+  const dim3 g(args.tiles_n * args.tiles_d, args.experts, args.splits), b(kThreads), j((unsigned)(args.tiles_n * args.tiles_d * 4));
+  if (args.transposed) hipLaunchKernelGGL((wgrad_near_kernel<DT, FMT, true>), g, b, 0, s, args);
+  else hipLaunchKernelGGL((wgrad_near_kernel<DT, FMT, false>), g, b, 0, s, args);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || args.splits <= 1) return e;
+  if (args.transposed) hipLaunchKernelGGL(wgrad_near_join_kernel<true>, j, b, 0, s, args);
+  else hipLaunchKernelGGL(wgrad_near_join_kernel<false>, j, b, 0, s, args);
+  return hipGetLastError();
+}
+
 hipError_t launch_wgrad(const WgradArgs &args, int dtype, int format, hipStream_t s) {
-  if (args.wide) {
-    if (dtype == kF16) return format == MUON_E4M3 ? launch_wide<kF16, MUON_E4M3>(args, s) : launch_wide<kF16, MUON_INT8>(args, s);
-    return format == MUON_E4M3 ? launch_wide<kBF16, MUON_E4M3>(args, s) : launch_wide<kBF16, MUON_INT8>(args, s);
-  }
-  const dim3 g(args.tiles_n * args.tiles_d, args.experts, args.splits), b(kThreads);
-#define MUON_WGRAD(DT, FMT)                                                                             \
-  if (args.transposed) hipLaunchKernelGGL((wgrad_kernel<DT, FMT, true>), g, b, 0, s, args);             \
-  else hipLaunchKernelGGL((wgrad_kernel<DT, FMT, false>), g, b, 0, s, args);                            \
-  break;
+#define MUON_WGRAD(DT, FMT) return args.wide ? launch_wide<DT, FMT>(args, s) : launch_near<DT, FMT>(args, s);
   switch (dtype * 2 + format) {
     case kF16 * 2 + MUON_E4M3: MUON_WGRAD(kF16, MUON_E4M3)
     case kF16 * 2 + MUON_INT8: MUON_WGRAD(kF16, MUON_INT8)
@@ -867,13 +904,6 @@ hipError_t launch_wgrad(const WgradArgs &args, int dtype, int format, hipStream_
     default: return hipErrorInvalidValue;
   }
 #undef MUON_WGRAD
-  return hipGetLastError();
-}
-
-hipError_t launch_wgrad_join(const WgradArgs &args, hipStream_t s) {
-  const int64_t size = (int64_t)args.outs * args.cols;
-  hipLaunchKernelGGL(wgrad_join_kernel, dim3((unsigned)((size + 1023) / 1024)), dim3(256), 0, s, args);
-  return hipGetLastError();
 }
 
 }  // namespace muon

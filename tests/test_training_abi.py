@@ -219,7 +219,6 @@ hipError_t launch_ckpt_unpack(const CkptArgs &, int, int, hipStream_t) { return 
 hipError_t launch_ckpt_swiglu(const CkptArgs &, int, int, hipStream_t) { return hipErrorNotSupported; }
 hipError_t launch_ckpt_swiglu_backward(const CkptArgs &, int, int, hipStream_t) { return hipErrorNotSupported; }
 hipError_t launch_wgrad(const WgradArgs &, int, int, hipStream_t) { return hipErrorNotSupported; }
-hipError_t launch_wgrad_join(const WgradArgs &, hipStream_t) { return hipErrorNotSupported; }
 hipError_t launch_route(const RouteArgs &, int, hipStream_t) { return hipErrorNotSupported; }
 hipError_t launch_route_backward(const RouteArgs &, int, hipStream_t) { return hipErrorNotSupported; }
 hipError_t launch_balance(float *, const void *, int, int64_t, int, float, hipStream_t) { return hipErrorNotSupported; }
