@@ -196,8 +196,10 @@ void plan_near(const muon_wgrad *a, WgradPlan &p) {
     const int64_t len = std::max<int64_t>(ceil_div(ceil_div(a->slots, s), 4 * kWgradK), 1) * 4 * kWgradK;
     if (s > 1 && ceil_div(a->slots, len) != s) continue;
     const int64_t blocks = tiles * s * E;
-    const double rounds = std::max((double)blocks / 768, 1.0);
-    double t = rounds * ((double)ceil_div(ceil_div(len, E), 4 * kWgradK) * 0.45e-6 + 1.5e-6) + 2e-6;
+    // measured: a step of a block's four waves 0.8 us and 3 us around them where
+    // blocks have room, 1.15 and 3 where two share each CU
+    const double rounds = std::max((double)blocks / 512, 1.0), busy = std::min((double)blocks / 512, 1.0);
+    double t = rounds * ((double)ceil_div(ceil_div(len, E), 4 * kWgradK) * (0.8e-6 + 0.35e-6 * busy) + 3e-6) + 2e-6;
     if (s > 1) t += (double)(tiles * s) * 64 * 64 * 8 / 4.5e12 + 3e-6;
     if (t < p.time) p.time = t, p.splits = (int)s, p.split_len = len;
   }

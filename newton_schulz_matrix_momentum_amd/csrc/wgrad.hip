@@ -87,14 +87,6 @@ __device__ __forceinline__ void slot_range(const Args &args, int e, int64_t &lo,
   }
 }
 
-// Checkpoint row of a slot, -1: left out
-__device__ __forceinline__ int64_t row_of(const WgradArgs &args, int64_t slot, int64_t hi) {
-  if (slot >= hi) return -1;
-  if (!args.rows_of) return slot;
-  const int r = args.rows_of[slot];
-  return (r >= 0 && r < args.ckpt_rows) ? (int64_t)r : (int64_t)-1;
-}
-
 template <int OT>
 __device__ __forceinline__ void put4(void *out, int64_t at, int n, bool vec, bool accumulate, f32x4 v) {
   typedef typename Val<OT>::type T;
@@ -684,85 +676,116 @@ constexpr int kNear = 64;
 __device__ __forceinline__ int near_key(int r) { return ((r >> 1) & 1) | ((r >> 2) & 2); }
 
 // output row and first of 4 columns of accumulator (i, k)
-template <bool TRANS>
-__device__ __forceinline__ void near_place(int n0, int d0, int lane, int f, int &r, int &c) {
+__device__ __forceinline__ void near_place(bool trans, int n0, int d0, int lane, int f, int &r, int &c) {
   // i: the MFMA's rows, contiguous in the output; k: its columns
   const int i = f >> 2, k = f & 3;
-  r = (TRANS ? d0 : n0) + 16 * k + (lane & 15);
-  c = (TRANS ? n0 : d0) + 16 * i + 4 * (lane >> 4);
+  r = (trans ? d0 : n0) + 16 * k + (lane & 15);
+  c = (trans ? n0 : d0) + 16 * i + 4 * (lane >> 4);
 }
 
-template <int DT, int FMT, bool TRANS>
-__global__ __launch_bounds__(kThreads, 3) void wgrad_near_kernel(WgradArgs args) {
+template <int DT, int FMT, bool GATHER, int END>
+__global__ __launch_bounds__(kThreads, 2) void wgrad_near_kernel(WgradArgs args) {
   typedef typename Val<DT>::type T;
   constexpr int ROW = kNear * 2, STAGE = kWgradK * ROW;          // 4 KB an operand
   __shared__ __attribute__((aligned(16))) char lds[4 * 2 * STAGE];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int tn = blockIdx.x / args.tiles_d, td = blockIdx.x % args.tiles_d;
+  // Blocks go to the 8 XCDs in turn, and each XCD has an L2 of its own: each takes
+  // one run of the parts' tiles (of an expert's tiles), so that little is read twice.
+  const unsigned n = gridDim.x * gridDim.z, at = blockIdx.x + gridDim.x * blockIdx.z, xcd = at & 7;
+  const unsigned v = xcd * (n >> 3) + min(xcd, n & 7) + (at >> 3);
+  const int part = v / gridDim.x, tile = v - part * gridDim.x;
+  const int tn = tile / args.tiles_d, td = tile - tn * args.tiles_d;
   const int n0 = tn * kNear, d0 = td * kNear;
   int64_t lo, hi;
   slot_range(args, blockIdx.y, lo, hi);
   if (args.splits > 1) {
-    lo += blockIdx.z * args.split_len;
+    lo += part * args.split_len;
     hi = min(hi, lo + args.split_len);
   }
+  // slots from here on count from lo; without rows to read there is nothing to add
+  const uint32_t len = hi > lo && args.ckpt_rows > 0 ? (uint32_t)(hi - lo) : 0;
   char *const ybuf = lds + wave * 2 * STAGE, *const xbuf = ybuf + STAGE;
 
+  // Loads stand outside all branches, so that a step's rows arrive while the two
+  // before it are multiplied: a slot past the end or left out reads a row that is
+  // there, and counts as zero in both operands (grad_y's row may hold anything).
+  // Columns past the matrix end in results that are not stored.
   // dy: lane covers row lane / 8 + 8 i, 8 columns from 8 (lane % 8)
   const int y_row = lane >> 3, y_col = (lane & 7) * 8;
-  const int y_n = min(args.outs - (n0 + y_col), 8);
-  const T *dy = (const T *)args.dy + n0 + y_col;
+  // END 1: the chunk that crosses a row's end is read from 8 columns before the end
+  // and shifted down.  END 2: rows shorter than a chunk are read by elements.
+  const bool crosses = n0 + y_col < args.outs && n0 + y_col + 8 > args.outs;
+  const T *const dy = (const T *)args.dy + lo * args.ld_dy + (END == 2 ? 0 : min(n0 + y_col, args.outs - 8));
   // x^: lane covers row lane / 4 + 16 i, 16 columns from 16 (lane % 4)
   const int x_row = lane >> 2, x_col = (lane & 3) * 16;
-  const bool x_in = d0 + x_col < args.cols;
-  const uint8_t *codes = args.codes + d0 + x_col, *scales = args.scales + (d0 + x_col) / kCkptBlock;
-  u32x4 ry[4], rx[2];
-  uint32_t rb[2];
-  auto fetch = [&](int64_t base) {
+  const int x_at = d0 + x_col < args.cols ? d0 + x_col : d0;
+  const int64_t first = GATHER ? 0 : lo;
+  const uint8_t *codes = args.codes + first * args.codes_ld + x_at, *scales = args.scales + first * args.scales_ld + x_at / kCkptBlock;
+  struct Rows {
+    u32x4 y[4], x[2];
+    uint32_t b[2];
+    int32_t row_y[4], row_x[2];                                  // GATHER: the slots' rows
+  };
+  const int32_t *const rows_of = GATHER ? args.rows_of + lo : nullptr;
+  // a slot past the end stands for the last: len > 0 wherever this is called
+  auto held = [&](uint32_t slot) { return min(slot, len - 1); };
+  auto fetch_rows = [&](uint32_t base, Rows &s) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t slot = base + y_row + 8 * i;
-      ry[i] = u32x4{};
-      if (y_n > 0 && row_of(args, slot, hi) >= 0) {
-        const T *p = dy + slot * args.ld_dy;
-        if (y_n == 8) {
-          ry[i] = *(const u32x4u *)p;
-        } else {
-          uint16_t t[8] = {};
+    for (int i = 0; i < 4; ++i) s.row_y[i] = rows_of[held(base + y_row + 8 * i)];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < y_n) t[k] = __builtin_bit_cast(uint16_t, p[k]);
+    for (int i = 0; i < 2; ++i) s.row_x[i] = rows_of[held(base + x_row + 16 * i)];
+  };
+  auto there = [&](int32_t r) { return r >= 0 && r < args.ckpt_rows; };
+  auto fetch = [&](uint32_t base, Rows &s) {
+    if constexpr (END != 2) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) ry[i][k] = (uint32_t)t[2 * k] | ((uint32_t)t[2 * k + 1] << 16);
-        }
-      }
+      for (int i = 0; i < 4; ++i) s.y[i] = *(const u32x4u *)(dy + (int64_t)held(base + y_row + 8 * i) * args.ld_dy);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t r = row_of(args, base + x_row + 16 * i, hi);
-      rx[i] = u32x4{};
-      rb[i] = 127;
-      if (r >= 0 && x_in) {
-        rx[i] = *(const u32x4 *)(codes + r * args.codes_ld);
-        rb[i] = scales[r * args.scales_ld];
-      }
+      int64_t r = held(base + x_row + 16 * i);
+      if constexpr (GATHER) r = there(s.row_x[i]) ? s.row_x[i] : 0;
+      s.x[i] = *(const u32x4 *)(codes + r * args.codes_ld);
+      s.b[i] = scales[r * args.scales_ld];
     }
   };
-  auto stage = [&]() {
+  auto stage = [&](uint32_t base, const Rows &s) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = y_row + 8 * i;
-      *(u32x4 *)(ybuf + r * ROW + ((((lane & 7) >> 1) ^ near_key(r)) * 32) + (lane & 1) * 16) = ry[i];
+      bool in = base + r < len;
+      if constexpr (GATHER) in = in && there(s.row_y[i]);
+      u32x4 y = {};
+      if constexpr (END != 2) y = s.y[i];
+      if constexpr (END == 1) {
+        const int drop = 16 * (8 - (args.outs & 7));             // 16 .. 112 bits
+        uint64_t a = (uint64_t)y[1] << 32 | y[0], b = (uint64_t)y[3] << 32 | y[2];
+        a = drop < 64 ? a >> drop | b << (64 - drop) : b >> (drop - 64);
+        b = drop < 64 ? b >> drop : 0;
+        if (crosses) y = u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+      }
+      if constexpr (END == 2) {
+        const T *p = dy + (int64_t)held(base + r) * args.ld_dy;
+        for (int k = 0; crosses && k < args.outs; ++k) {
+          const uint32_t v = (uint32_t)__builtin_bit_cast(uint16_t, p[k]) << (16 * (k & 1));
+#pragma unroll
+          for (int h = 0; h < 4; ++h) y[h] |= k >> 1 == h ? v : 0;
+        }
+      }
+      *(u32x4 *)(ybuf + r * ROW + ((((lane & 7) >> 1) ^ near_key(r)) * 32) + (lane & 1) * 16) = in ? y : u32x4{};
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = x_row + 16 * i;
+      bool in = base + r < len;
+      if constexpr (GATHER) in = in && there(s.row_x[i]);
       u32x4 a, b;
-      decode16<DT, FMT>(rx[i], rb[i], a, b);
+      __builtin_amdgcn_sched_barrier(0);
+      decode16<DT, FMT>(s.x[i], s.b[i], a, b);
       char *p = xbuf + r * ROW + (((lane & 3) ^ near_key(r)) * 32);
-      *(u32x4 *)p = a;
-      *(u32x4 *)(p + 16) = b;
+      *(u32x4 *)p = in ? a : u32x4{};
+      *(u32x4 *)(p + 16) = in ? b : u32x4{};
     }
   };
   const int r0 = 8 * (lane >> 4) + ((lane & 15) >> 2);          // near_key(r0 + 4) is near_key(r0)
@@ -775,23 +798,54 @@ __global__ __launch_bounds__(kThreads, 3) void wgrad_near_kernel(WgradArgs args)
   };
 
   f32x4 acc[16] = {};
-  int64_t base = lo + wave * kWgradK;
-  if (base < hi) fetch(base);
-  for (; base < hi; base += 4 * kWgradK) {                       // wave-uniform
-    stage();
-    if (base + 4 * kWgradK < hi) fetch(base + 4 * kWgradK);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    u32x4 fy[4], fx[4];
+  constexpr uint32_t STEP = 4 * kWgradK;
+  uint32_t base = wave * kWgradK;
+  Rows ahead[2], after;
+  const char *const rows_buf = args.transposed ? ybuf : xbuf, *const cols_buf = args.transposed ? xbuf : ybuf;
+  auto step = [&](Rows &s, auto go_on) {
+    constexpr bool more = decltype(go_on)::value != 0;
+    stage(base, s);
+    __builtin_amdgcn_sched_barrier(0);          // keeps registers under 256
+    if constexpr (GATHER && more) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) fy[i] = frag(ybuf, i), fx[i] = frag(xbuf, i);
+      for (int i = 0; i < 4; ++i) s.row_y[i] = after.row_y[i];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) s.row_x[i] = after.row_x[i];
+    }
+    if constexpr (more) fetch(base + 2 * STEP, s);
+    if constexpr (GATHER && more) fetch_rows(base + 3 * STEP, after);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    u32x4 fa[4], fb[4];                                          // the MFMA's rows and columns
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fa[i] = frag(rows_buf, i), fb[i] = frag(cols_buf, i);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if constexpr (TRANS) mma<DT>(fy[i], fx[k], acc[4 * i + k]);
-        else mma<DT>(fx[i], fy[k], acc[4 * i + k]);
-      }
+      for (int k = 0; k < 4; ++k) mma<DT>(fa[i], fb[k], acc[4 * i + k]);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    base += STEP;
+  };
+  if (base < len) {                                              // wave-uniform
+    if constexpr (GATHER) fetch_rows(base, ahead[0]);
+    if (base + STEP < len) {
+      if constexpr (GATHER) {
+        fetch_rows(base + STEP, ahead[1]);
+        fetch_rows(base + 2 * STEP, after);
+      }
+      __builtin_amdgcn_sched_barrier(0);        // in this order: the loop waits by count
+      fetch(base, ahead[0]);
+      __builtin_amdgcn_sched_barrier(0);
+      fetch(base + STEP, ahead[1]);
+      __builtin_amdgcn_sched_barrier(0);
+      do {
+        step(ahead[0], IntC<1>());
+        step(ahead[1], IntC<1>());
+      } while (base + STEP < len);
+    } else {
+      fetch(base, ahead[0]);
+    }
+    if (base < len) step(ahead[0], IntC<0>());
   }
 
   // the waves' sums, 16 KB each, in the two halves of LDS
@@ -810,26 +864,25 @@ __global__ __launch_bounds__(kThreads, 3) void wgrad_near_kernel(WgradArgs args)
     }
   }
   __syncthreads();
-  const int rows = TRANS ? args.cols : args.outs, width = TRANS ? args.outs : args.cols;
+  const int rows = args.transposed ? args.cols : args.outs, width = args.transposed ? args.outs : args.cols;
   const bool split = args.splits > 1;
   const bool vec = (width & 3) == 0 && (((uintptr_t)args.out) & 15) == 0;
-#pragma unroll
+#pragma unroll 1                                                 // short code: a launch fetches it anew
   for (int q = 0; q < 4; ++q) {
     const int f = 4 * wave + q;
-    const f32x4 v = ((f32x4 *)lds)[f * 64 + lane] + ((f32x4 *)lds)[(16 + f) * 64 + lane];
+    const f32x4 sum = ((f32x4 *)lds)[f * 64 + lane] + ((f32x4 *)lds)[(16 + f) * 64 + lane];
     if (split) {
-      *(f32x4 *)(args.part + ((((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * 16 + f) * 64 + lane) * 4) = v;
+      *(f32x4 *)(args.part + (((int64_t)v * 16 + f) * 64 + lane) * 4) = sum;
       continue;
     }
     int r, c;
-    near_place<TRANS>(n0, d0, lane, f, r, c);
+    near_place(args.transposed, n0, d0, lane, f, r, c);
     if (r < rows && c < width)
-      put4_any(args.out, args.out_dtype, (int64_t)blockIdx.y * args.outs * args.cols + (int64_t)r * width + c, min(width - c, 4), vec, args.accumulate, v);
+      put4_any(args.out, args.out_dtype, (int64_t)blockIdx.y * args.outs * args.cols + (int64_t)r * width + c, min(width - c, 4), vec, args.accumulate, sum);
   }
 }
 
 // out = (out +) the sum of the parts, in their order: a wave a fragment of a tile
-template <bool TRANS>
 __global__ __launch_bounds__(kThreads) void wgrad_near_join_kernel(WgradArgs args) {
   const int tiles = args.tiles_n * args.tiles_d, lane = threadIdx.x & 63;
   const int t = blockIdx.x / 4, f = (blockIdx.x % 4) * 4 + (threadIdx.x >> 6);
@@ -844,9 +897,9 @@ __global__ __launch_bounds__(kThreads) void wgrad_near_join_kernel(WgradArgs arg
     for (int i = 0; i < 4; ++i) v += a[i];
   }
   for (; p < args.splits; ++p) v += *(const f32x4 *)(src + (int64_t)p * tiles * 16 * 256);
-  const int rows = TRANS ? args.cols : args.outs, width = TRANS ? args.outs : args.cols;
+  const int rows = args.transposed ? args.cols : args.outs, width = args.transposed ? args.outs : args.cols;
   int r, c;
-  near_place<TRANS>(t / args.tiles_d * kNear, t % args.tiles_d * kNear, lane, f, r, c);
+  near_place(args.transposed, t / args.tiles_d * kNear, t % args.tiles_d * kNear, lane, f, r, c);
   if (r < rows && c < width)
     put4_any(args.out, args.out_dtype, (int64_t)r * width + c, min(width - c, 4), (width & 3) == 0 && (((uintptr_t)args.out) & 15) == 0, args.accumulate, v);
 }
@@ -885,12 +938,20 @@ hipError_t launch_wide(const WgradArgs &args, hipStream_t s) {
 template <int DT, int FMT>
 hipError_t launch_near(const WgradArgs &args, hipStream_t s) {
   const dim3 g(args.tiles_n * args.tiles_d, args.experts, args.splits), b(kThreads), j((unsigned)(args.tiles_n * args.tiles_d * 4));
-  if (args.transposed) hipLaunchKernelGGL((wgrad_near_kernel<DT, FMT, true>), g, b, 0, s, args);
-  else hipLaunchKernelGGL((wgrad_near_kernel<DT, FMT, false>), g, b, 0, s, args);
+  const int end = args.outs < 8 ? 2 : args.outs % 8 ? 1 : 0;
+#define MUON_NEAR(GATHER, END) hipLaunchKernelGGL((wgrad_near_kernel<DT, FMT, GATHER, END>), g, b, 0, s, args)
+  switch (end * 2 + (args.rows_of ? 1 : 0)) {
+    case 0: MUON_NEAR(false, 0); break;
+    case 1: MUON_NEAR(true, 0); break;
+    case 2: MUON_NEAR(false, 1); break;
+    case 3: MUON_NEAR(true, 1); break;
+    case 4: MUON_NEAR(false, 2); break;
+    default: MUON_NEAR(true, 2); break;
+  }
+#undef MUON_NEAR
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || args.splits <= 1) return e;
-  if (args.transposed) hipLaunchKernelGGL(wgrad_near_join_kernel<true>, j, b, 0, s, args);
-  else hipLaunchKernelGGL(wgrad_near_join_kernel<false>, j, b, 0, s, args);
+  hipLaunchKernelGGL(wgrad_near_join_kernel, j, b, 0, s, args);
   return hipGetLastError();
 }
 
