@@ -95,6 +95,9 @@ __device__ __forceinline__ void store4(typename Val<DT>::type *p, int n, const f
   }
 }
 
+// n of v[0 .. 8) to p, past the caches: nothing here reads them again (16384 x
+// 2816 bf16 SwiGLU 72 -> 68 us, its backward 82 -> 76 us; streaming loads and
+// codes as well gained nothing)
 template <int DT>
 __device__ __forceinline__ void store8(typename Val<DT>::type *p, int n, const float (&v)[8]) {
   if (n >= 8) {
@@ -102,15 +105,15 @@ __device__ __forceinline__ void store8(typename Val<DT>::type *p, int n, const f
       f32x4u a, b;
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[i] = v[i], b[i] = v[4 + i];
-      *(f32x4u *)p = a;
-      *(f32x4u *)(p + 4) = b;
+      __builtin_nontemporal_store(a, (f32x4u *)p);
+      __builtin_nontemporal_store(b, (f32x4u *)(p + 4));
     } else {
       u32x4u a;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         a[i] = (uint32_t)__builtin_bit_cast(uint16_t, Val<DT>::from(v[2 * i])) |
                ((uint32_t)__builtin_bit_cast(uint16_t, Val<DT>::from(v[2 * i + 1])) << 16);
-      *(u32x4u *)p = a;
+      __builtin_nontemporal_store(a, (u32x4u *)p);
     }
   } else {
 #pragma unroll
