@@ -423,7 +423,7 @@ muon_status muon_route_backward(const muon_routing *args, const float *grad_weig
 
 /* Balance of the experts by their bias, which takes no gradient: per layer
  *     bias[e] += rate * sign(mean over experts of counts - counts[e])
- * (compared in whole numbers).  bias and counts are layers x experts,
+ * (compared in whole numbers).  bias and counts are layers (at most 2^23) x experts,
  * contiguous; counts is int32 (count_bytes 4) or int64 (8), each >= 0. */
 muon_status muon_balance_step(float *bias, const void *counts, int count_bytes, int64_t layers, int64_t experts, float rate,
                               void *stream);

@@ -162,7 +162,8 @@ constexpr int64_t kWidePart = int64_t(256) * 128 * 4;
 // partials pass memory twice at 4.5 TB/s and their join costs a launch.
 bool plan_wide(const muon_wgrad *a, WgradPlan &p) {
   const int64_t N = a->outs, D = a->ckpt.cols, E = a->experts;
-  if (N % 8 != 0 || a->slots == 0 || a->ckpt.rows == 0) return false;
+  // (slots are counted in 32 bits, a stage past the end included)
+  if (N % 8 != 0 || a->slots == 0 || a->slots > (int64_t(1) << 30) || a->ckpt.rows == 0) return false;
   const int64_t waste1 = ceil_div(N, 256) * 256 * ceil_div(D, 128) * 128, waste2 = ceil_div(N, 128) * 128 * ceil_div(D, 256) * 256;
   // (int8 codes keep to one chunk a thread: two fill the registers past 256,
   // 2048 x 1408 x 64 experts 532 us against 400 with 9% more padding)
@@ -185,8 +186,11 @@ bool plan_wide(const muon_wgrad *a, WgradPlan &p) {
   return true;
 }
 
-// 64 x 64 tiles, four waves that share a block's steps, three blocks a CU:
-// near 1.5 us to start and store a round, 0.45 us a wave's step.
+// 64 x 64 tiles, four waves that share a block's steps, two blocks a CU.  As
+// measured, a block takes 3 us around its steps; a step of its waves (128
+// slots) takes 0.8 us while blocks have room and 1.15 where two share each CU.
+// By these estimates 2048 slots of 1024 x 1024 take these tiles (17 us, wide
+// ones 27) and 16384 of 2816 x 1024 the wide ones (118 us, these 199).
 void plan_near(const muon_wgrad *a, WgradPlan &p) {
   const int64_t E = a->experts;
   p.tiles_n = ceil_div(a->outs, 64);
@@ -196,8 +200,6 @@ void plan_near(const muon_wgrad *a, WgradPlan &p) {
     const int64_t len = std::max<int64_t>(ceil_div(ceil_div(a->slots, s), 4 * kWgradK), 1) * 4 * kWgradK;
     if (s > 1 && ceil_div(a->slots, len) != s) continue;
     const int64_t blocks = tiles * s * E;
-    // measured: a step of a block's four waves 0.8 us and 3 us around them where
-    // blocks have room, 1.15 and 3 where two share each CU
     const double rounds = std::max((double)blocks / 512, 1.0), busy = std::min((double)blocks / 512, 1.0);
     double t = rounds * ((double)ceil_div(ceil_div(len, E), 4 * kWgradK) * (0.8e-6 + 0.35e-6 * busy) + 3e-6) + 2e-6;
     if (s > 1) t += (double)(tiles * s) * 64 * 64 * 8 / 4.5e12 + 3e-6;
@@ -482,7 +484,7 @@ muon_status muon_balance_step(float *bias, const void *counts, int count_bytes, 
   if (layers < 0 || experts < 1) return fail(MUON_ERR_INVALID_ARG, "layers must be >= 0 and experts >= 1");
   if (count_bytes != 4 && count_bytes != 8) return fail(MUON_ERR_UNSUPPORTED, "counts are int32 (4) or int64 (8), got %d bytes", count_bytes);
   if (!std::isfinite(rate)) return fail(MUON_ERR_INVALID_ARG, "rate is not finite");
-  if (layers > kMaxRows || experts > kMaxCols) return fail(MUON_ERR_UNSUPPORTED, "%lld x %lld exceeds the supported size", (long long)layers, (long long)experts);
+  if (layers > (1 << 23) || experts > kMaxCols) return fail(MUON_ERR_UNSUPPORTED, "%lld x %lld exceeds the supported size", (long long)layers, (long long)experts);
   if (layers == 0) return done();
   if (!bias || !counts) return fail(MUON_ERR_INVALID_ARG, "bias and counts must be non-NULL");
   if ((((uintptr_t)counts) & (uintptr_t)(count_bytes - 1)) || (((uintptr_t)bias) & 3))

@@ -271,6 +271,67 @@ def test_wgrad_of_experts(nsm, outs, cols, dtype, transposed):
     assert (kept[0] == 3).all() and (kept[3] == 3).all()
 
 
+@pytest.mark.parametrize("tokens,outs,cols", [(130, 2056, 2072), (130, 2176, 2300), (8137, 1032, 1000), (8137, 904, 1270)])
+@pytest.mark.parametrize("dtype,fmt,out_dtype,transposed", [("bf16", "e4m3", "bf16", False), ("f16", "int8", "f32", True),
+                                                            ("bf16", "int8", "f16", True), ("f16", "e4m3", "f32", False)])
+def test_wgrad_of_large_matrices(nsm, tokens, outs, cols, dtype, fmt, out_dtype, transposed):
+    """Sizes that fill the device with large tiles, the longer ones in parts;
+    a block of x that is marked reaches its 32 columns and no other."""
+    x, dy = activations(tokens, cols, dtype, 7), (0.1 * activations(tokens, outs, dtype, 8).float()).to(DT[dtype])
+    c = nsm.checkpoint_pack(x.cuda(), format=fmt)
+    xq = operand(ref.checkpoint(to64(x), fmt)[0], dtype)
+    want, size = to64(dy).T @ xq, np.abs(to64(dy)).T @ np.abs(xq)
+    if transposed:
+        want, size = want.T, size.T
+    tol = half_step(want, out_dtype) + (tokens + 4) * U32 * size
+    got = nsm.checkpoint_wgrad(dy.cuda(), c, out_dtype=DT[out_dtype], transposed=transposed)
+    near(got, want, tol, "dW")
+    again = nsm.checkpoint_wgrad(strided(dy.cuda(), outs + 1), c, out_dtype=DT[out_dtype], transposed=transposed)
+    near(again, want, tol, "dW of unaligned rows")
+    base = activations(*got.shape, out_dtype, 9).cuda()
+    total = to64(base) + want
+    nsm.checkpoint_wgrad(dy.cuda(), c, out=base, transposed=transposed, accumulate=True)
+    near(base, total, tol + half_step(total, out_dtype) + U32 * np.abs(total), "dW added")
+    c.scales[tokens - 1, 3] = 255
+    c.codes[tokens - 1, 96:128] = 0
+    bad = nsm.checkpoint_wgrad(dy.cuda(), c, out_dtype=DT[out_dtype], transposed=transposed)
+    bad, got = (bad.T, got.T) if transposed else (bad, got)
+    assert torch.isnan(bad[:, 96:128]).all()
+    assert torch.equal(bad[:, :96], got[:, :96]) and torch.equal(bad[:, 128:], got[:, 128:])
+
+
+@pytest.mark.parametrize("dtype,fmt", [("bf16", "e4m3"), ("f16", "int8")])
+@pytest.mark.parametrize("experts,outs,cols,pad", [(70, 520, 500, 0), (70, 264, 500, 0), (6, 1032, 1000, 0), (16, 904, 1270, 0),
+                                                   (5, 5, 40, 0), (5, 8, 33, 0), (5, 61, 100, 0), (3, 64, 64, 3)])
+def test_wgrad_of_uneven_experts(nsm, experts, outs, cols, pad, dtype, fmt):
+    """One expert has most slots, several none; rows are picked with repeats and
+    some are left out, whose grad_y rows hold infinities and NaN; more experts
+    than a wave has lanes; outs below and beside a vector; unaligned rows (pad)."""
+    tokens, slots = 200, 900
+    gen = torch.Generator().manual_seed(experts + outs)
+    cuts = torch.sort(torch.randint(0, slots // 3, (experts - 1,), generator=gen)).values
+    cuts[1::3] = cuts[0::3][:len(cuts[1::3])]                        # empty experts
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int64), torch.sort(cuts).values, torch.tensor([slots - 7])]).to(torch.int32)
+    rows = torch.randint(0, tokens, (slots,), generator=gen, dtype=torch.int32)
+    x, dy = activations(tokens, cols, dtype, 12), (0.1 * activations(slots, outs, dtype, 13).float()).to(DT[dtype])
+    clean = to64(dy)
+    for i, (row, value) in {2: (-1, math.inf), slots - 8: (tokens, math.nan), slots - 9: (-7, -math.inf), 450: (2 ** 31 - 1, math.nan)}.items():
+        rows[i], dy[i], clean[i] = row, value, 0.0
+    dy[slots - 7:], clean[slots - 7:] = math.nan, 0.0                # behind the last expert
+    c = nsm.checkpoint_pack(x.cuda(), format=fmt)
+    xq = operand(ref.checkpoint(to64(x), fmt)[0], dtype)
+    picked = xq[rows.clamp(0, tokens - 1).numpy()]                   # left-out slots meet zeros in clean
+    runs = [slice(int(a), int(b)) for a, b in zip(offsets[:-1], offsets[1:])]
+    want = np.stack([clean[r].T @ picked[r] for r in runs])
+    size = np.stack([np.abs(clean[r]).T @ np.abs(picked[r]) for r in runs])
+    tol = half_step(want, "f32") + (slots + 4) * U32 * size
+    view = strided(dy.cuda(), outs + pad) if pad else dy.cuda()
+    got = nsm.checkpoint_wgrad(view, c, offsets=offsets.cuda(), rows=rows.cuda())
+    near(got, want, tol, "dW of experts")
+    turned = nsm.checkpoint_wgrad(view, c, offsets=offsets.cuda(), rows=rows.cuda(), transposed=True)
+    near(turned, want.transpose(0, 2, 1), tol.transpose(0, 2, 1), "dW of experts, transposed")
+
+
 def test_wgrad_offsets_out_of_range_are_clamped(nsm):
     x, dy = activations(40, 32, "bf16", 1), activations(40, 32, "bf16", 2)
     c = nsm.checkpoint_pack(x.cuda())
@@ -303,6 +364,24 @@ def test_wgrad_rows_far_apart(nsm):
     dy.copy_(small)
     c = nsm.checkpoint_pack(activations(tokens, cols, "bf16", 4).cuda())
     assert torch.equal(nsm.checkpoint_wgrad(dy, c), nsm.checkpoint_wgrad(small, c))
+
+
+def test_codes_far_apart(nsm):
+    """Code rows 2^27 bytes apart: 40 rows pass 2^32 bytes."""
+    ld, tokens, outs, cols = 1 << 27, 40, 264, 300
+    wide = torch.empty(tokens * ld, dtype=torch.uint8, device="cuda")
+    codes = wide.as_strided((tokens, 304), (ld, 1))
+    x = activations(tokens, cols, "bf16", 5).cuda()
+    far = nsm.Checkpoint(codes, torch.empty(tokens, 10, dtype=torch.uint8, device="cuda"), cols)
+    nsm.checkpoint_pack(x, out=far)
+    close = nsm.checkpoint_pack(x)
+    assert torch.equal(far.codes, close.codes) and torch.equal(far.scales, close.scales)
+    assert torch.equal(nsm.checkpoint_unpack(far), nsm.checkpoint_unpack(close))
+    dy = activations(tokens, outs, "bf16", 6).cuda()
+    assert torch.equal(nsm.checkpoint_wgrad(dy, far), nsm.checkpoint_wgrad(dy, close))
+    rows = torch.arange(tokens - 1, -1, -1, dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, 17, tokens], dtype=torch.int32, device="cuda")
+    assert torch.equal(nsm.checkpoint_wgrad(dy, far, rows=rows, offsets=offsets), nsm.checkpoint_wgrad(dy, close, rows=rows, offsets=offsets))
 
 
 # ---------------------------------------------------------------- routing
