@@ -1,14 +1,20 @@
 // Routing of tokens to experts: choice, weights and dispatch lists, the
 // gradient of the weights, and the bias step that balances the experts.
 //
-// Forward: a wave takes a token, expert lane + 64 r in register r of a lane.
+// Forward: a wave takes four tokens, a row of 16 lanes each (one token where
+// there are more than 256 experts, 16 picks or 16 groups).
 // Choices are what 64-bit arithmetic says, found in 32 bits wherever those
 // decide: logits order the experts exactly; of score + bias, a pick counts
 // only where its lead over the next choice passes twice the 32-bit error, and
 // a token with a closer pair (about one in 500 of 256 sigmoid scores) is done
-// again in 64 bits.  A pick is a maximum over registers, six cross-lane moves
-// and a ballot, with no LDS.  Weights need the taken logits alone and are
-// computed for all of them at once.
+// again in 64 bits.  A pick is a maximum over registers and a few cross-lane
+// moves, with no LDS.  Weights need the taken logits alone and are computed
+// for all of them at once.
+//
+// The issue of vector instructions bounds it, not memory: 16384 tokens of 256
+// sigmoid scores in 8 groups with bias take 28 us and 10 for the lists (17 MB;
+// 220 us with a wave a token in 64 bits), 32768 tokens of 64 softmax scores 24
+// us in all, 5 tokens 5.8 us in one launch.
 //
 // The lists are a counting sort by expert that keeps the slots' order: each
 // block counts its own slots, one block an expert turns the counts into the
@@ -817,7 +823,8 @@ __device__ __forceinline__ float pick_gradient(const RouteArgs &args, bool have,
 }
 
 // Up to 256 experts and 16 picks: four tokens a wave, in the layout of the
-// forward kernel; lane j of a row holds pick j.
+// forward kernel; lane j of a row holds pick j.  32768 tokens of 64 bf16 scores:
+// 6.9 us for 10 MB (20 us with a wave a token).
 template <int DT, int V>
 __global__ __launch_bounds__(kThreads) void route_rows_backward_kernel(RouteArgs args) {
   typedef typename Val<DT>::type T;

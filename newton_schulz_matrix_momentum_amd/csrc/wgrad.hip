@@ -151,6 +151,14 @@ __device__ __forceinline__ void place(int n0, int d0, int wave, int lane, int i,
 // is read; then one barrier, behind which stage i + 1 is complete and stage
 // i's buffers are free; then products of the second half while stage i + 1's
 // first fragments are read and the buffers are refilled.
+//
+// The matrix instructions and the LDS reads that feed them bound it.  Measured:
+// 16384 tokens, 4096 x 4096, 1.1 - 1.2 PFLOP/s (a library bf16 product of
+// 8192^3 reaches 1.23); 16384 tokens, 2816 x 1024, 109 us and 12 for its join
+// (94 GFLOP: 88 tiles in 5 parts leave 72 of the 512 places empty); 64 experts
+// of 1408 x 2048 over 49152 picked rows 400 - 460 us (283 GFLOP and 369 MB of
+// results).  One part of 128 x 128 a block, without the DMA ring, took 216 us
+// at 2816 x 1024.
 constexpr int kRing = 4;
 constexpr uint64_t kRowBits = 0x0101010101010101ull;
 
@@ -665,9 +673,11 @@ __global__ __launch_bounds__(kThreads) void wgrad_wide_join_kernel(WgradArgs arg
 // (odd widths, unaligned strides): 64 outs x 64 columns per block.  The block's
 // four waves take its steps of 32 tokens in turn, each for the whole tile, in
 // LDS of its own, so the loop has no barrier: rows go global -> registers ->
-// LDS, fragments come back through transposing reads, and the next step's
+// LDS, fragments come back through transposing reads, and the next two steps'
 // rows are on their way meanwhile.  The waves' sums meet in LDS at the end
-// ((0 + 2) + (1 + 3)).  Many small blocks hide the latency that bounds this.
+// ((0 + 2) + (1 + 3)).  The latency of a few steps bounds it: 8192 tokens of
+// 192 x 768 take 15 us in 13 parts and 4 for the join, 8 experts of 333 x 517
+// over 602 picked rows 12 us (17 and 16 with one step ahead, behind branches).
 //
 // LDS rows are 128 bytes; the 32-byte chunk c of row r is kept at c ^ near_key(r):
 // of the 8 rows that half a wave reads at once, the four of equal parity have
