@@ -12,9 +12,9 @@
 // for all of them at once.
 //
 // The issue of vector instructions bounds it, not memory: 16384 tokens of 256
-// sigmoid scores in 8 groups with bias take 28 us and 10 for the lists (17 MB;
-// 220 us with a wave a token in 64 bits), 32768 tokens of 64 softmax scores 24
-// us in all, 5 tokens 5.8 us in one launch.
+// sigmoid scores in 8 groups with bias take 18 us on warm data, 25 on cold, and
+// 10 for the lists (17 MB; 220 us in all with a wave a token in 64 bits), 32768
+// tokens of 64 softmax scores 24 us in all, 5 tokens 5.8 us in one launch.
 //
 // The lists are a counting sort by expert that keeps the slots' order: each
 // block counts its own slots, one block an expert turns the counts into the
@@ -474,12 +474,16 @@ __device__ __forceinline__ void each(F &&f) {
 
 constexpr int kRedo = -2;
 
-// The groups that stay, as a bit at g * p for group g (p lanes share a group),
+// a / b of small numbers (below 2^20, b >= 1): a + 1/2 stays 1 / (2 b) away from
+// every multiple of b, which two roundings of 2^-23 do not bridge
+__device__ __forceinline__ int small_quotient(int a, int b) { return (int)(((float)a + 0.5f) * __builtin_amdgcn_rcpf((float)b)); }
+
+// The groups that stay, as a bit at g << lp for group g (2^lp lanes share a group),
 // and by how much the last of them is ahead of the first that goes.
 template <typename F, int V>
-__device__ __forceinline__ uint32_t row_groups(const RouteArgs &args, const F (&c)[V], F *choice, int p, int lane, F &lead) {
+__device__ __forceinline__ uint32_t row_groups(const RouteArgs &args, const F (&c)[V], F *choice, int lp, int lane, F &lead) {
   const F none = -(F)INFINITY;
-  const int E = args.experts, l16 = lane & 15, size = E / args.groups, g = l16 / p, sub = l16 % p;
+  const int E = args.experts, l16 = lane & 15, p = 1 << lp, size = small_quotient(E, args.groups), g = l16 >> lp, sub = l16 & (p - 1);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = (v >> 2) * 64 + l16 * 4 + (v & 3);
@@ -487,9 +491,9 @@ __device__ __forceinline__ uint32_t row_groups(const RouteArgs &args, const F (&
   }
   wave_sync();
   F a = none, b = none;
-  const int n = (size - sub + p - 1) / p;       // this lane's choices, from a place of its own: distinct banks
+  const int n = (size - sub + p - 1) >> lp;     // this lane's choices, from a place of its own: distinct banks
   if (g < args.groups && n > 0) {
-    int at = l16 % n;
+    int at = l16 - small_quotient(l16, n) * n;
     for (int i = 0; i < n; ++i) {
       const F x = choice[g * size + sub + at * p];
       b = fmax(b, fmin(a, x));
@@ -507,7 +511,7 @@ __device__ __forceinline__ uint32_t row_groups(const RouteArgs &args, const F (&
   if (score != score) score = none;             // inf - inf
   int rank = 0;
   for (int i = 0; i < args.groups; ++i) {
-    const F other = __shfl(score, (lane & 48) + i * p, 64);
+    const F other = __shfl(score, (lane & 48) + (i << lp), 64);
     rank += other > score || (other == score && i < g) ? 1 : 0;
   }
   const bool mine = g < args.groups && sub == 0, in = mine && rank < args.top_groups;
@@ -534,17 +538,24 @@ __global__ __launch_bounds__(512, 4) void route_rows_kernel(RouteArgs args) {
   const int rows = (int)min(args.tokens - t0, (int64_t)args.rows_per_block);
 
   // where an expert's group stands, 4 bits a register; the bias's largest
-  int p = 1;
+  int lp = 0;
   uint32_t shift[(V + 7) / 8] = {};
   float bias_top = 0.0f;
   if (grouped) {
-    while (2 * p * args.groups <= 16) p *= 2;
-    const int size = E / args.groups;
+    while ((args.groups << (lp + 1)) <= 16) ++lp;
+    const int size = small_quotient(E, args.groups);
 #pragma unroll
-    for (int v = 0; v < V; ++v) shift[v / 8] |= (uint32_t)(min((v >> 2) * 64 + l16 * 4 + (v & 3), E - 1) / size * p) << (4 * (v & 7));
+    for (int v = 0; v < V; ++v) shift[v / 8] |= (uint32_t)(small_quotient(min((v >> 2) * 64 + l16 * 4 + (v & 3), E - 1), size) << lp) << (4 * (v & 7));
   }
   if (biased) {
-    for (int e = l16; e < E; e += 16) bias_top = fmaxf(bias_top, fabsf(args.bias[e]));
+    float b[V / 4][4];                          // (all on their way at once)
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) load4<kF32>(args.bias + i * 64 + l16 * 4, E - i * 64 - l16 * 4, b[i]);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float x = b[v >> 2][v & 3];         // -inf: none, or an expert that is never taken
+      bias_top = fmaxf(bias_top, x == -INFINITY ? 0.0f : fabsf(x));
+    }
     bias_top = __uint_as_float(row_max(__float_as_uint(bias_top)));
   }
 
@@ -602,7 +613,7 @@ __global__ __launch_bounds__(512, 4) void route_rows_kernel(RouteArgs args) {
     bool close = false;
     if (grouped) {
       float lead;
-      stay = row_groups<float, V>(args, c, (float *)scratch + (threadIdx.x >> 4) * E, p, lane, lead);
+      stay = row_groups<float, V>(args, c, (float *)scratch + (threadIdx.x >> 4) * E, lp, lane, lead);
       close = !(lead > 2.0f * wanted);          // a score is a sum of two choices
     }
     // Keys of 24 bits with the expert in the other 8, so that each is its own
