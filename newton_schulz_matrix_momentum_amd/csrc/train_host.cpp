@@ -196,16 +196,18 @@ void plan_near(const muon_wgrad *a, WgradPlan &p) {
   p.tiles_n = ceil_div(a->outs, 64);
   p.tiles_d = ceil_div(a->ckpt.cols, 64);
   const int64_t tiles = p.tiles_n * p.tiles_d;
-  for (int64_t s = 1; s <= (a->offsets || a->slots == 0 ? 1 : 64); ++s) {
-    const int64_t len = std::max<int64_t>(ceil_div(ceil_div(a->slots, s), 4 * kWgradK), 1) * 4 * kWgradK;
-    if (s > 1 && ceil_div(a->slots, len) != s) continue;
+  for (int64_t s = 1; s <= (a->slots == 0 ? 1 : 64); ++s) {
+    // an expert's parts are formed where its length is known; here all are alike
+    const int64_t share = ceil_div(a->slots, E);
+    const int64_t len = std::max<int64_t>(ceil_div(ceil_div(share, s), 4 * kWgradK), 1) * 4 * kWgradK;
+    if (s > 1 && ceil_div(share, len) != s) continue;
     const int64_t blocks = tiles * s * E;
     const double rounds = std::max((double)blocks / 512, 1.0), busy = std::min((double)blocks / 512, 1.0);
-    double t = rounds * ((double)ceil_div(ceil_div(len, E), 4 * kWgradK) * (0.8e-6 + 0.35e-6 * busy) + 3e-6) + 2e-6;
-    if (s > 1) t += (double)(tiles * s) * 64 * 64 * 8 / 4.5e12 + 3e-6;
+    double t = rounds * ((double)(len / (4 * kWgradK)) * (0.8e-6 + 0.35e-6 * busy) + 3e-6) + 2e-6;
+    if (s > 1) t += (double)blocks * 64 * 64 * 8 / 4.5e12 + 3e-6;
     if (t < p.time) p.time = t, p.splits = (int)s, p.split_len = len;
   }
-  if (p.splits > 1) p.bytes = (size_t)(p.splits * tiles) * 64 * 64 * 4;
+  if (p.splits > 1) p.bytes = (size_t)(p.splits * tiles * E) * 64 * 64 * 4;
 }
 
 WgradPlan plan_wgrad(const muon_wgrad *a) {

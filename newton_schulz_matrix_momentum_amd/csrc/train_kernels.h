@@ -64,13 +64,13 @@ struct WgradArgs {
   const int32_t *offsets;
   const int32_t *rows_of;
   void *out;               // final matrices
-  float *part;             // fp32 partials (splits > 1), [split][outs * cols]
+  float *part;             // fp32 partials (splits > 1) of tiles, by part, expert and tile
   int64_t ld_dy, codes_ld, scales_ld;
   int64_t slots, ckpt_rows;
   int32_t outs, cols;
   int32_t experts;
-  int32_t splits;          // parts of the token range (1 expert only when > 1)
-  int64_t split_len;       // tokens of one part, a multiple of the k step
+  int32_t splits;          // parts of the token range, or (64 x 64 tiles) of each expert's slots
+  int64_t split_len;       // tokens of one part without offsets, a multiple of the k step
   int32_t tiles_n, tiles_d;
   int32_t out_dtype;
   int32_t accumulate;

@@ -113,6 +113,18 @@ __device__ __forceinline__ void put4_any(void *out, int dtype, int64_t at, int n
   else put4<kF16>(out, at, n, vec, acc, v);
 }
 
+template <int OT>
+__device__ __forceinline__ void put1(void *out, int64_t at, bool accumulate, float v) {
+  typename Val<OT>::type *p = (typename Val<OT>::type *)out + at;
+  *p = Val<OT>::from(accumulate ? v + Val<OT>::to(*p) : v);
+}
+
+__device__ __forceinline__ void put1_any(void *out, int dtype, int64_t at, bool acc, float v) {
+  if (dtype == kF32) put1<kF32>(out, at, acc, v);
+  else if (dtype == kBF16) put1<kBF16>(out, at, acc, v);
+  else put1<kF16>(out, at, acc, v);
+}
+
 constexpr int kThreads = 256;
 
 // LDS rows of a wide tile hold one token's values of one operand; the 32-byte
@@ -678,6 +690,8 @@ __global__ __launch_bounds__(kThreads) void wgrad_wide_join_kernel(WgradArgs arg
 // ((0 + 2) + (1 + 3)).  The latency of a few steps bounds it: 8192 tokens of
 // 192 x 768 take 15 us in 13 parts and 4 for the join, 8 experts of 333 x 517
 // over 602 picked rows 12 us (17 and 16 with one step ahead, behind branches).
+// Long sums over few tiles are split, an expert's too (9 of 152 x 74 over 33354
+// slots 44 -> 20 us with the join).
 //
 // LDS rows are 128 bytes; the 32-byte chunk c of row r is kept at c ^ near_key(r):
 // of the 8 rows that half a wave reads at once, the four of equal parity have
@@ -702,16 +716,19 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_near_kernel(WgradArgs args)
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Blocks go to the 8 XCDs in turn, and each XCD has an L2 of its own: each takes
   // one run of the parts' tiles (of an expert's tiles), so that little is read twice.
-  const unsigned n = gridDim.x * gridDim.z, at = blockIdx.x + gridDim.x * blockIdx.z, xcd = at & 7;
+  const bool one = gridDim.y == 1;
+  const unsigned n = gridDim.x * (one ? gridDim.z : 1), at = blockIdx.x + (one ? gridDim.x * blockIdx.z : 0), xcd = at & 7;
   const unsigned v = xcd * (n >> 3) + min(xcd, n & 7) + (at >> 3);
-  const int part = v / gridDim.x, tile = v - part * gridDim.x;
+  const int part = one ? v / gridDim.x : blockIdx.z, tile = one ? v - part * gridDim.x : v;
   const int tn = tile / args.tiles_d, td = tile - tn * args.tiles_d;
   const int n0 = tn * kNear, d0 = td * kNear;
   int64_t lo, hi;
   slot_range(args, blockIdx.y, lo, hi);
   if (args.splits > 1) {
-    lo += part * args.split_len;
-    hi = min(hi, lo + args.split_len);
+    // an expert's length is known here alone: equal parts of its own slots
+    const int64_t len = args.offsets ? ((hi - lo + args.splits - 1) / args.splits + 4 * kWgradK - 1) / (4 * kWgradK) * (4 * kWgradK) : args.split_len;
+    lo = min(lo + part * len, hi);
+    hi = min(hi, lo + len);
   }
   // slots from here on count from lo; without rows to read there is nothing to add
   const uint32_t len = hi > lo && args.ckpt_rows > 0 ? (uint32_t)(hi - lo) : 0;
@@ -877,41 +894,55 @@ __global__ __launch_bounds__(kThreads, 2) void wgrad_near_kernel(WgradArgs args)
   const int rows = args.transposed ? args.cols : args.outs, width = args.transposed ? args.outs : args.cols;
   const bool split = args.splits > 1;
   const bool vec = (width & 3) == 0 && (((uintptr_t)args.out) & 15) == 0;
+  if (split || vec) {
 #pragma unroll 1                                                 // short code: a launch fetches it anew
-  for (int q = 0; q < 4; ++q) {
-    const int f = 4 * wave + q;
-    const f32x4 sum = ((f32x4 *)lds)[f * 64 + lane] + ((f32x4 *)lds)[(16 + f) * 64 + lane];
-    if (split) {
-      *(f32x4 *)(args.part + (((int64_t)v * 16 + f) * 64 + lane) * 4) = sum;
-      continue;
+    for (int q = 0; q < 4; ++q) {
+      const int f = 4 * wave + q;
+      const f32x4 sum = ((f32x4 *)lds)[f * 64 + lane] + ((f32x4 *)lds)[(16 + f) * 64 + lane];
+      if (split) {
+        *(f32x4 *)(args.part + ((((int64_t)part * gridDim.y + blockIdx.y) * gridDim.x + tile) * 16 + f) * 256 + lane * 4) = sum;
+        continue;
+      }
+      int r, c;
+      near_place(args.transposed, n0, d0, lane, f, r, c);
+      if (r < rows && c < width)
+        put4_any(args.out, args.out_dtype, (int64_t)blockIdx.y * args.outs * args.cols + (int64_t)r * width + c, min(width - c, 4), vec, args.accumulate, sum);
     }
-    int r, c;
-    near_place(args.transposed, n0, d0, lane, f, r, c);
-    if (r < rows && c < width)
-      put4_any(args.out, args.out_dtype, (int64_t)blockIdx.y * args.outs * args.cols + (int64_t)r * width + c, min(width - c, 4), vec, args.accumulate, sum);
+    return;
+  }
+  // rows that 4 columns do not divide: a wave a row, a lane a column (6 matrices
+  // of 825 x 2737 in fp32: 42 us by fours, 36 here)
+  const int r0w = (args.transposed ? d0 : n0) + 16 * wave, c = (args.transposed ? n0 : d0) + lane;
+  const float *const at_lane = (const float *)lds + ((4 * (lane >> 4) + wave) * 64 + ((lane >> 2) & 3) * 16) * 4 + (lane & 3);
+  if (c < width) {
+#pragma unroll 1
+    for (int q = 0; q < 16 && r0w + q < rows; ++q)
+      put1_any(args.out, args.out_dtype, (int64_t)blockIdx.y * args.outs * args.cols + (int64_t)(r0w + q) * width + c, args.accumulate,
+               at_lane[4 * q] + at_lane[16 * 256 + 4 * q]);
   }
 }
 
 // out = (out +) the sum of the parts, in their order: a wave a fragment of a tile
 __global__ __launch_bounds__(kThreads) void wgrad_near_join_kernel(WgradArgs args) {
   const int tiles = args.tiles_n * args.tiles_d, lane = threadIdx.x & 63;
+  const int64_t stride = (int64_t)tiles * args.experts * 16 * 256;             // between parts
   const int t = blockIdx.x / 4, f = (blockIdx.x % 4) * 4 + (threadIdx.x >> 6);
-  const float *src = args.part + (((int64_t)t * 16 + f) * 64 + lane) * 4;
+  const float *src = args.part + ((((int64_t)blockIdx.y * tiles + t) * 16 + f) * 64 + lane) * 4;
   f32x4 v = {};
   int p = 0;
   for (; p + 4 <= args.splits; p += 4) {        // four loads on their way
     f32x4 a[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = *(const f32x4 *)(src + (int64_t)(p + i) * tiles * 16 * 256);
+    for (int i = 0; i < 4; ++i) a[i] = *(const f32x4 *)(src + (p + i) * stride);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v += a[i];
   }
-  for (; p < args.splits; ++p) v += *(const f32x4 *)(src + (int64_t)p * tiles * 16 * 256);
+  for (; p < args.splits; ++p) v += *(const f32x4 *)(src + p * stride);
   const int rows = args.transposed ? args.cols : args.outs, width = args.transposed ? args.outs : args.cols;
   int r, c;
   near_place(args.transposed, t / args.tiles_d * kNear, t % args.tiles_d * kNear, lane, f, r, c);
   if (r < rows && c < width)
-    put4_any(args.out, args.out_dtype, (int64_t)r * width + c, min(width - c, 4), (width & 3) == 0 && (((uintptr_t)args.out) & 15) == 0, args.accumulate, v);
+    put4_any(args.out, args.out_dtype, (int64_t)blockIdx.y * args.outs * args.cols + (int64_t)r * width + c, min(width - c, 4), (width & 3) == 0 && (((uintptr_t)args.out) & 15) == 0, args.accumulate, v);
 }
 
 }  // namespace
@@ -947,7 +978,7 @@ hipError_t launch_wide(const WgradArgs &args, hipStream_t s) {
 
 template <int DT, int FMT>
 hipError_t launch_near(const WgradArgs &args, hipStream_t s) {
-  const dim3 g(args.tiles_n * args.tiles_d, args.experts, args.splits), b(kThreads), j((unsigned)(args.tiles_n * args.tiles_d * 4));
+  const dim3 g(args.tiles_n * args.tiles_d, args.experts, args.splits), b(kThreads), j((unsigned)(args.tiles_n * args.tiles_d * 4), args.experts);
   const int end = args.outs < 8 ? 2 : args.outs % 8 ? 1 : 0;
 #define MUON_NEAR(GATHER, END) hipLaunchKernelGGL((wgrad_near_kernel<DT, FMT, GATHER, END>), g, b, 0, s, args)
   switch (end * 2 + (args.rows_of ? 1 : 0)) {

@@ -332,6 +332,39 @@ def test_wgrad_of_uneven_experts(nsm, experts, outs, cols, pad, dtype, fmt):
     near(turned, want.transpose(0, 2, 1), tol.transpose(0, 2, 1), "dW of experts, transposed")
 
 
+@pytest.mark.parametrize("out_dtype,transposed", [("f32", False), ("bf16", True), ("f16", False)])
+@pytest.mark.parametrize("experts,outs,cols", [(4, 61, 50), (3, 72, 66), (1, 130, 33), (2, 7, 259)])
+def test_wgrad_of_long_experts(nsm, experts, outs, cols, out_dtype, transposed):
+    """Few tiles and many slots: an expert's slots are summed in parts; one
+    expert has hardly any, one none; rows of the result that 4 columns do not divide."""
+    slots = 6001
+    cuts = {1: [0, slots - 3], 2: [5, 5, slots], 3: [0, 5000, 5001, slots], 4: [0, 2900, 2900, 2930, slots]}[experts]
+    offsets = torch.tensor(cuts, dtype=torch.int32)
+    x, dy = activations(slots, cols, "bf16", 14), (0.1 * activations(slots, outs, "bf16", 15).float()).to(torch.bfloat16)
+    c = nsm.checkpoint_pack(x.cuda())
+    dy64, xq = to64(dy), ref.checkpoint(to64(x), "e4m3")[0]
+    runs = [slice(a, b) for a, b in zip(cuts[:-1], cuts[1:])]
+    want, size = (np.stack([m(dy64[r]).T @ m(xq[r]) for r in runs]) for m in (np.asarray, np.abs))
+    if transposed:
+        want, size = want.transpose(0, 2, 1), size.transpose(0, 2, 1)
+    tol = half_step(want, out_dtype) + (slots + 4) * U32 * size
+    got = nsm.checkpoint_wgrad(dy.cuda(), c, offsets=offsets.cuda(), out_dtype=DT[out_dtype], transposed=transposed)
+    near(got, want, tol, "dW of long experts")
+    base = torch.stack([activations(*got.shape[1:], out_dtype, 16 + e) for e in range(experts)]).cuda()
+    before = base.clone()
+    total = to64(base) + want
+    nsm.checkpoint_wgrad(dy.cuda(), c, out=base, offsets=offsets.cuda(), transposed=transposed, accumulate=True)
+    near(base, total, tol + half_step(total, out_dtype) + U32 * np.abs(total), "dW added")
+    for e, r in enumerate(runs):
+        if r.start == r.stop:
+            assert not got[e].any() and torch.equal(base[e], before[e])
+    # one allocation to the other's side: nothing is written behind the matrices
+    flat = torch.full((got.numel() + 64,), 5.0, dtype=DT[out_dtype], device="cuda")
+    nsm.checkpoint_wgrad(dy.cuda(), c, out=flat[1:got.numel() + 1].view(got.shape), offsets=offsets.cuda(), transposed=transposed)
+    assert (flat[0] == 5) and (flat[got.numel() + 1:] == 5).all()
+    near(flat[1:got.numel() + 1].view(got.shape), want, tol, "dW in an unaligned place")
+
+
 def test_wgrad_offsets_out_of_range_are_clamped(nsm):
     x, dy = activations(40, 32, "bf16", 1), activations(40, 32, "bf16", 2)
     c = nsm.checkpoint_pack(x.cuda())
